@@ -361,6 +361,133 @@ int sharq_linear_grouped(const sharq_act *a, const int *d_group_offsets, const s
                          void *d_Y, int out_dtype, void *d_ws, size_t ws_bytes,
                          sharq_stream_t stream);
 
+/*
+ * ---------------------------------------------------------------------------
+ * The 8-bit path: linear layers kept in E4M3 (sign, 4 exponent, 3 mantissa
+ * bits, largest value 448) with one float32 scale per row and 128 columns of
+ * an activation and per 128 x 128 block of a weight.  It stands beside the FP4
+ * path for the layers a model keeps in 8 bits (the reviews' comparator, FP8)
+ * and reads checkpoints in that layout as they are: plain row-major codes, no
+ * packing.
+ *
+ * Shapes: K (H, I) % 16 == 0 and at most 1<<17; D any from 1 to 1<<18; rows
+ * and columns may end inside a block.  T from 0 to 1<<22.  Strides (ld*) are
+ * in elements.  bf16 inputs are read in 16-byte pieces: their base must lie on
+ * 16 bytes and their stride be a multiple of 8.
+ * Non-finite inputs: a NaN stays a NaN of its own; an infinity makes its
+ * 128-block NaN.  They reach the outputs that depend on them and no others.
+ * All kernels are launched as programmatic dependents and read nothing before
+ * the preceding kernel of the stream has completed.
+ * ---------------------------------------------------------------------------
+ */
+
+/* codes: E4M3 [E][D][K] (K contiguous), scales: float32
+ * [E][ceil(D/128)][ceil(K/128)]; the weight is code * scale. */
+typedef struct {
+  void *codes;
+  float *scales;
+  int K, D, E;
+} sharq_fp8_weight;
+
+/* codes: E4M3 [T][K]; scales: float32 [ceil(K/128)][lds], the scale of row t
+ * and block b at b * lds + t (lds >= T, a multiple of 4; entries past T are
+ * neither read nor written). */
+typedef struct {
+  void *codes;
+  float *scales;
+  int T, K, lds;
+} sharq_fp8_act;
+
+/* Host-only size queries (0 on an invalid shape) and views of a caller-owned
+ * buffer of that size, as for the FP4 operands.  A caller that has codes and
+ * scales already fills the structs itself (16-byte aligned codes and
+ * activation scales). */
+size_t sharq_fp8_weight_bytes(int K, int D, int E);
+size_t sharq_fp8_act_bytes(int T, int K);
+int sharq_fp8_weight_view(void *d_buf, int K, int D, int E, sharq_fp8_weight *out);
+int sharq_fp8_act_view(void *d_buf, int T, int K, sharq_fp8_act *out);
+
+/*
+ * sharq_fp8_pack_weight - quantize W (bf16 [E][K][D] row-major) into w.
+ * Per 128 x 128 block: s = max|W| / 448 (at least 2^-126; 1 for a block of
+ * zeros), code = e4m3_rn(f32(W * f32(1/s))).
+ */
+int sharq_fp8_pack_weight(const void *d_W, const sharq_fp8_weight *w, sharq_stream_t stream);
+
+/*
+ * sharq_fp8_prep - the preparation of an activation for the 8-bit path.
+ * d_X: bf16 [a->T] rows of a->K, row stride ldx.  d_gamma: bf16 [K] RMSNorm
+ * weight, or NULL for an input that is not normalised.
+ *   v = x * (1/sqrt(mean(x^2) + eps)) * gamma   (v = x without gamma), float32
+ *   per row and 128 columns: s = max|v| / 448 (at least 2^-126; 1 for a block
+ *   of zeros), code = e4m3_rn(f32(v * f32(1/s)))
+ * v is not rounded to bf16 first, unlike Xn of the FP4 path.  A row of zeros
+ * with eps = 0 is NaN, as the formula is.
+ */
+int sharq_fp8_prep(const void *d_X, int64_t ldx, const void *d_gamma, float eps, const sharq_fp8_act *a,
+                   sharq_stream_t stream);
+
+/*
+ * sharq_fp8_prep_residual - the same of h = bf16_rn(f32(x) + f32(res)), the
+ * updated residual stream, which is written to d_res_out unless that is NULL.
+ * d_res_out may be d_res itself (with ldo == ldr); it must not overlap d_X,
+ * nor d_res in any other way (SHARQ_ERR_INVALID_ARG).
+ */
+int sharq_fp8_prep_residual(const void *d_X, int64_t ldx, const void *d_res, int64_t ldr, void *d_res_out,
+                            int64_t ldo, const void *d_gamma, float eps, const sharq_fp8_act *a,
+                            sharq_stream_t stream);
+
+/*
+ * sharq_fp8_prep_silu_mul - the same of v = silu(gate) * up (float32, not
+ * rounded in between), the input of a down projection.  The two may be the
+ * halves of one gate+up output (ldg = ldu = 2 K).
+ */
+int sharq_fp8_prep_silu_mul(const void *d_gate, int64_t ldg, const void *d_up, int64_t ldu, const sharq_fp8_act *a,
+                            sharq_stream_t stream);
+
+/*
+ * sharq_fp8_linear - Y = X W:
+ *   Y[t][d] = sum over 128-blocks b of xs[t][b] ws[d/128][b] *
+ *             (sum over k in b of x[t][k] w[d][k])
+ * products and sums in float32, rounded once to out_dtype.  w->E == 1.  d_Y:
+ * [T][D], row stride ldy >= D, aligned to its elements (16-byte aligned rows
+ * are stored faster).  d_ws: at least sharq_fp8_linear_workspace_bytes, zeroed
+ * once by the caller; it holds the error word that sharq_check_status reads.
+ * The result does not depend on timing: sums split over K are joined in a
+ * fixed order.
+ */
+size_t sharq_fp8_linear_workspace_bytes(int T, int K, int D);
+int sharq_fp8_linear(const sharq_fp8_act *a, const sharq_fp8_weight *w, void *d_Y, int64_t ldy, int out_dtype,
+                     void *d_ws, size_t ws_bytes, sharq_stream_t stream);
+
+/*
+ * sharq_fp8_moe - a whole mixture-of-experts layer for a few tokens (decode),
+ * in two kernels.  Larger batches belong to a grouped GEMM.
+ *   chosen(t): the topk largest of d_logits[t][0..E-1] (float32, row stride
+ *     ldl), equal logits by the lower index.
+ *   p(t, j): softmax over the chosen logits (renormalize != 0) or the chosen
+ *     entries of the softmax over all E (renormalize == 0).  A logit of -inf
+ *     or NaN gives p = 0 (NaN sorts below -inf); a token without any other
+ *     logit gets y = 0.
+ *   y[t] = sum_j p(t, j) W2_e (silu(Wg_e x_t) * (Wu_e x_t)),  e = chosen(t)[j]
+ * w13: E experts of D = 2 I rows, the gate's I rows and then the up's, K = H;
+ * w2: E experts of D = H, K = I.  d_X: bf16 [T][H], row stride ldx; activations
+ * are not quantized.  h is float32 and multiplied as f16 with a power-of-two
+ * scale per 128 (2^-11 relative).  d_Y: bf16 [T][H], row stride ldy; it may be
+ * d_X.  d_topk_ids (int32) and d_topk_weights (float32), [T][topk]: written
+ * unless NULL.
+ * T <= 64, topk <= 16 and <= E, E <= 512 (SHARQ_ERR_UNSUPPORTED_SHAPE).
+ * d_ws: at least sharq_fp8_moe_workspace_bytes (no initial value); calls that
+ * may run at the same time need one each.
+ */
+#define SHARQ_FP8_MOE_MAX_T 64
+#define SHARQ_FP8_MOE_MAX_TOPK 16
+#define SHARQ_FP8_MOE_MAX_E 512
+size_t sharq_fp8_moe_workspace_bytes(int T, int topk, int H, int I, int E);
+int sharq_fp8_moe(const void *d_X, int64_t ldx, const float *d_logits, int64_t ldl, int T, int topk, int renormalize,
+                  const sharq_fp8_weight *w13, const sharq_fp8_weight *w2, void *d_Y, int64_t ldy,
+                  int32_t *d_topk_ids, float *d_topk_weights, void *d_ws, size_t ws_bytes, sharq_stream_t stream);
+
 /* Synchronises `stream`, returns the device-side error word of d_ws
  * (SHARQ_OK if none) and clears it. */
 int sharq_check_status(void *d_ws, sharq_stream_t stream);

@@ -25,6 +25,11 @@ __all__ = [
     "sharq_status_string", "sharq_abi_version", "sharq_prep_noalloc", "sharq_prep_linear", "prep_linear",
     "sharq_prep_residual", "sharq_prep_silu_mul",
     "PackedWeight", "PreparedAct", "Workspace", "linear", "EXPORTED_SYMBOLS",
+    "SharqFp8Weight", "SharqFp8Act", "SHARQ_FP8_MOE_MAX_T", "SHARQ_FP8_MOE_MAX_TOPK", "SHARQ_FP8_MOE_MAX_E",
+    "sharq_fp8_weight_bytes", "sharq_fp8_act_bytes", "sharq_fp8_weight_view", "sharq_fp8_act_view",
+    "sharq_fp8_pack_weight", "sharq_fp8_prep", "sharq_fp8_prep_residual", "sharq_fp8_prep_silu_mul",
+    "sharq_fp8_linear_workspace_bytes", "sharq_fp8_linear", "sharq_fp8_moe_workspace_bytes", "sharq_fp8_moe",
+    "Fp8Weight", "Fp8Act", "Fp8Workspace", "fp8_linear", "fp8_moe",
 ]
 
 SHARQ_MODE_SHARQ = 0
@@ -39,6 +44,9 @@ SHARQ_FMT_NVFP4 = 0
 SHARQ_FMT_MXFP4 = 1
 SHARQ_OUT_BF16 = 0
 SHARQ_OUT_F32 = 1
+SHARQ_FP8_MOE_MAX_T = 64
+SHARQ_FP8_MOE_MAX_TOPK = 16
+SHARQ_FP8_MOE_MAX_E = 512
 
 EXPORTED_SYMBOLS = (
     "sharq_weight_bytes", "sharq_act_bytes", "sharq_workspace_bytes", "sharq_weight_view",
@@ -46,6 +54,9 @@ EXPORTED_SYMBOLS = (
     "sharq_check_status", "sharq_status_string", "sharq_abi_version", "sharq_prep_noalloc",
     "sharq_prep_linear", "sharq_weight_bytes_fmt", "sharq_weight_view_fmt", "sharq_prep_residual",
     "sharq_prep_silu_mul",
+    "sharq_fp8_weight_bytes", "sharq_fp8_act_bytes", "sharq_fp8_weight_view", "sharq_fp8_act_view",
+    "sharq_fp8_pack_weight", "sharq_fp8_prep", "sharq_fp8_prep_residual", "sharq_fp8_prep_silu_mul",
+    "sharq_fp8_linear_workspace_bytes", "sharq_fp8_linear", "sharq_fp8_moe_workspace_bytes", "sharq_fp8_moe",
 )
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -74,6 +85,16 @@ class SharqAct(ctypes.Structure):
                 ("r_meta", ctypes.c_void_p)]
 
 
+class SharqFp8Weight(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("K", ctypes.c_int), ("D", ctypes.c_int),
+                ("E", ctypes.c_int)]
+
+
+class SharqFp8Act(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("T", ctypes.c_int), ("K", ctypes.c_int),
+                ("lds", ctypes.c_int)]
+
+
 def lib():
     """Load libsharq.so (in-tree build); raises if it has not been built."""
     global _lib
@@ -84,6 +105,7 @@ def lib():
         L = ctypes.CDLL(library_path)
         vp, i, sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
         W, A = ctypes.POINTER(SharqWeight), ctypes.POINTER(SharqAct)
+        ll, W8, A8 = ctypes.c_int64, ctypes.POINTER(SharqFp8Weight), ctypes.POINTER(SharqFp8Act)
         sig = {
             "sharq_weight_bytes": (sz, [i, i, i]),
             "sharq_act_bytes": (sz, [i, i, i]),
@@ -103,6 +125,18 @@ def lib():
             "sharq_check_status": (i, [vp, vp]),
             "sharq_status_string": (ctypes.c_char_p, [i]),
             "sharq_abi_version": (i, []),
+            "sharq_fp8_weight_bytes": (sz, [i, i, i]),
+            "sharq_fp8_act_bytes": (sz, [i, i]),
+            "sharq_fp8_weight_view": (i, [vp, i, i, i, W8]),
+            "sharq_fp8_act_view": (i, [vp, i, i, A8]),
+            "sharq_fp8_pack_weight": (i, [vp, W8, vp]),
+            "sharq_fp8_prep": (i, [vp, ll, vp, ctypes.c_float, A8, vp]),
+            "sharq_fp8_prep_residual": (i, [vp, ll, vp, ll, vp, ll, vp, ctypes.c_float, A8, vp]),
+            "sharq_fp8_prep_silu_mul": (i, [vp, ll, vp, ll, A8, vp]),
+            "sharq_fp8_linear_workspace_bytes": (sz, [i, i, i]),
+            "sharq_fp8_linear": (i, [A8, W8, vp, ll, i, vp, sz, vp]),
+            "sharq_fp8_moe_workspace_bytes": (sz, [i, i, i, i, i]),
+            "sharq_fp8_moe": (i, [vp, ll, vp, ll, i, i, i, W8, W8, vp, ll, vp, vp, vp, sz, vp]),
         }
         for name, (res, args) in sig.items():
             f = getattr(L, name)
@@ -202,6 +236,64 @@ def sharq_linear_grouped(a, d_offsets, w, d_Y, out_dtype, d_ws, ws_bytes, stream
 
 def sharq_check_status(d_ws, stream):
     return lib().sharq_check_status(d_ws, stream)
+
+
+def sharq_fp8_weight_bytes(K, D, E=1):
+    return lib().sharq_fp8_weight_bytes(K, D, E)
+
+
+def sharq_fp8_act_bytes(T, K):
+    return lib().sharq_fp8_act_bytes(T, K)
+
+
+def sharq_fp8_weight_view(d_buf, K, D, E=1):
+    w = SharqFp8Weight()
+    _check(lib().sharq_fp8_weight_view(d_buf, K, D, E, ctypes.byref(w)), "sharq_fp8_weight_view")
+    return w
+
+
+def sharq_fp8_act_view(d_buf, T, K):
+    a = SharqFp8Act()
+    _check(lib().sharq_fp8_act_view(d_buf, T, K, ctypes.byref(a)), "sharq_fp8_act_view")
+    return a
+
+
+def sharq_fp8_pack_weight(d_W, w, stream):
+    return _check(lib().sharq_fp8_pack_weight(d_W, ctypes.byref(w), stream), "sharq_fp8_pack_weight")
+
+
+def sharq_fp8_prep(d_X, ldx, d_gamma, eps, a, stream):
+    return _check(lib().sharq_fp8_prep(d_X, ldx, d_gamma, eps, ctypes.byref(a), stream), "sharq_fp8_prep")
+
+
+def sharq_fp8_prep_residual(d_X, ldx, d_res, ldr, d_res_out, ldo, d_gamma, eps, a, stream):
+    return _check(lib().sharq_fp8_prep_residual(d_X, ldx, d_res, ldr, d_res_out, ldo, d_gamma, eps, ctypes.byref(a),
+                                                stream), "sharq_fp8_prep_residual")
+
+
+def sharq_fp8_prep_silu_mul(d_gate, ldg, d_up, ldu, a, stream):
+    return _check(lib().sharq_fp8_prep_silu_mul(d_gate, ldg, d_up, ldu, ctypes.byref(a), stream),
+                  "sharq_fp8_prep_silu_mul")
+
+
+def sharq_fp8_linear_workspace_bytes(T, K, D):
+    return lib().sharq_fp8_linear_workspace_bytes(T, K, D)
+
+
+def sharq_fp8_linear(a, w, d_Y, ldy, out_dtype, d_ws, ws_bytes, stream):
+    return _check(lib().sharq_fp8_linear(ctypes.byref(a), ctypes.byref(w), d_Y, ldy, out_dtype, d_ws, ws_bytes, stream),
+                  "sharq_fp8_linear")
+
+
+def sharq_fp8_moe_workspace_bytes(T, topk, H, I, E):
+    return lib().sharq_fp8_moe_workspace_bytes(T, topk, H, I, E)
+
+
+def sharq_fp8_moe(d_X, ldx, d_logits, ldl, T, topk, renormalize, w13, w2, d_Y, ldy, d_topk_ids, d_topk_weights, d_ws,
+                  ws_bytes, stream):
+    return _check(lib().sharq_fp8_moe(d_X, ldx, d_logits, ldl, T, topk, renormalize, ctypes.byref(w13),
+                                      ctypes.byref(w2), d_Y, ldy, d_topk_ids, d_topk_weights, d_ws, ws_bytes, stream),
+                  "sharq_fp8_moe")
 
 # ------------------------------------------------- torch conveniences ------
 
@@ -348,3 +440,15 @@ def prep_linear(X, gamma, eps, weight, act=None, out_dtype=None, out=None, ws=No
                       act.view if act is not None else None, weight.view, out.data_ptr(), code,
                       ws.buf.data_ptr(), ws.nbytes, _stream_ptr(stream))
     return out
+
+
+_FP8_NAMES = ("Fp8Weight", "Fp8Act", "Fp8Workspace", "fp8_linear", "fp8_moe")
+
+
+def __getattr__(name):  # the 8-bit path's torch conveniences; torch is imported with them
+    if name in _FP8_NAMES:
+        from . import fp8
+        for n in _FP8_NAMES:
+            globals()[n] = getattr(fp8, n)
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

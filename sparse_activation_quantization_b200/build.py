@@ -14,7 +14,7 @@ import sys
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libsharq.so")
-SOURCES = ["api.cu", "prep.cu", "pack_weight.cu", "gemm.cu"]
+SOURCES = ["api.cu", "prep.cu", "pack_weight.cu", "gemm.cu", "fp8_api.cu", "fp8_prep.cu", "fp8_linear.cu", "fp8_moe.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC"]
 

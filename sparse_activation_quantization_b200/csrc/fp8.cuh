@@ -1,0 +1,205 @@
+// fp8.cuh - device helpers of the 8-bit (E4M3, block-scaled) path: format
+// conversion, the legacy warp-level matrix instructions that stream a weight
+// once, tensor-map copies and the 8-bit tcgen05 MMA.
+#pragma once
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "sharq_device.cuh"
+
+namespace sharq {
+namespace fp8 {
+
+constexpr int kBlock = 128;                 // elements (and weight columns) per scale
+constexpr float kE4m3Max = 448.0f;
+constexpr uint64_t kWaitNs = 4000000000ull;  // bound of every device-side wait: far beyond any tile's work
+constexpr int kErrTimeoutWord = -5;          // SHARQ_ERR_TIMEOUT
+
+__host__ __device__ __forceinline__ int blocks_of(int n) { return (n + kBlock - 1) / kBlock; }
+
+// s = max / 448, at least the smallest normal float (so 1/s is finite), 1 for
+// a block of zeros.  A NaN in the block is skipped by the maximum and keeps
+// its own code; an infinity makes s infinite and the block NaN.
+__device__ __forceinline__ float block_scale_e4m3(float amax) {
+  return amax > 0.0f ? fmaxf(__fdiv_rn(amax, kE4m3Max), 0x1p-126f) : 1.0f;
+}
+
+// four floats -> four E4M3 bytes, a in the lowest (round to nearest even,
+// saturating; NaN -> 0x7F)
+__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
+  uint32_t out;
+  asm("{\n\t.reg .b16 lo, hi;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 lo, %2, %1;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;\n\t"
+      "mov.b32 %0, {lo, hi};\n\t}"
+      : "=r"(out)
+      : "f"(a), "f"(b), "f"(c), "f"(d));
+  return out;
+}
+
+__device__ __forceinline__ void unpack_bf16x8(const uint4& v, float (&f)[8]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = __uint_as_float(w[i] << 16);
+    f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+  }
+}
+__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
+  const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&b);
+}
+__device__ __forceinline__ uint4 pack_bf16x8(const float (&f)[8]) {
+  return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                    pack_bf16x2(f[6], f[7]));
+}
+
+// silu(g) * u in float32: silu(g) = (g >= 0 ? g : g e^-|g|) / (1 + e^-|g|), so
+// the divisor stays in [1, 2] and nothing overflows; silu(-inf) = -0
+__device__ __forceinline__ float silu_mul(float g, float u) {
+  const float e = __expf(-fabsf(g));
+  return __fdividef(g >= 0.0f ? g : fmaxf(g, -200.0f) * e, 1.0f + e) * u;
+}
+
+// Programmatic dependent launch.  wait: the preceding grid has completed and
+// its memory is visible; trigger: the next grid may start its set-up.
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+__device__ __forceinline__ void record_error_word(int* err, int code) {
+  if (err) atomicCAS(err, 0, code);
+}
+
+// 16-byte load of bytes that are read once (weights)
+__device__ __forceinline__ uint4 ld_stream(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p)
+               : "memory");
+  return v;
+}
+
+// ---------------------------------------------- warp-level MMA (m16n8) ----
+
+// c += A (16 x 32 E4M3, row major) x B (32 x 8 E4M3): a0/a1 rows g, g+8 of
+// the lower 16 k, a2/a3 of the upper, b0/b1 likewise.  Any permutation of k
+// that A and B share gives the same sum.
+__device__ __forceinline__ void mma_e4m3(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// c += A (16 x 16 f16) x B (16 x 8 f16)
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// four E4M3 bytes -> two f16 pairs (exact)
+__device__ __forceinline__ void e4m3x4_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 l, h;\n\t"
+      "mov.b32 {l, h}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, l;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
+}
+__device__ __forceinline__ uint32_t f16x2_of(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// ------------------------------------------------- tensor-map copies ----
+
+// 2-D tile (c0: element along the contiguous axis, c1: row) -> shared memory,
+// bytes counted on `bar`
+__device__ __forceinline__ void tma_2d(void* dst, const CUtensorMap* map, int c0, int c1, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(
+          smem_u32(dst)),
+      "l"(map), "r"(smem_u32(bar)), "r"(c0), "r"(c1)
+      : "memory");
+}
+// the same from a CTA of a pair: `bar_cluster` may be the other CTA's barrier
+__device__ __forceinline__ void tma_2d_pair(void* dst, const CUtensorMap* map, int c0, int c1, uint32_t bar_cluster) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], "
+      "[%2];" ::"r"(smem_u32(dst)),
+      "l"(map), "r"(bar_cluster), "r"(c0), "r"(c1)
+      : "memory");
+}
+__device__ __forceinline__ void tma_prefetch_map(const CUtensorMap* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
+// hint: bring a tile into L2.  Nothing is read into the program, so it may run
+// before the preceding grid has completed.
+__device__ __forceinline__ void tma_prefetch_2d(const CUtensorMap* map, int c0, int c1) {
+  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(map), "r"(c0), "r"(c1)
+               : "memory");
+}
+
+// ------------------------------------------------------- tcgen05, 8-bit ----
+
+// Instruction descriptor of kind::f8f6f4: D float32 (1 in bits 4-5), A and B
+// E4M3 (0 in bits 7-9 and 10-12), both K-major, N >> 3 in bits 17-22, M >> 4
+// in bits 24-28.
+__host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N) {
+  return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+// D(tmem) (+)= A(smem) x B(smem), K = 32
+__device__ __forceinline__ void mma_f8(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void mma_f8_pair(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(acc)
+      : "memory");
+}
+
+// two independent float32 multiply-adds in one instruction: d = a * b + d
+__device__ __forceinline__ void fma2(float& d0, float& d1, float a0, float a1, float b) {
+  asm("{\n\t.reg .b64 d, a, b;\n\t"
+      "mov.b64 d, {%0, %1};\n\t"
+      "mov.b64 a, {%2, %3};\n\t"
+      "mov.b64 b, {%4, %4};\n\t"
+      "fma.rn.f32x2 d, a, b, d;\n\t"
+      "mov.b64 {%0, %1}, d;\n\t}"
+      : "+f"(d0), "+f"(d1)
+      : "f"(a0), "f"(a1), "f"(b));
+}
+
+// ----------------------------------------------------------- host side ----
+
+// device properties that the launchers need, looked up once per device
+struct Device {
+  int sms = 0;
+};
+// nullptr if the current device cannot be used
+const Device* device();
+// a kernel's attribute that is set once per device: `done` is the kernel's own table
+cudaError_t opt_in_smem(const void* kernel, int bytes, bool (&done)[64]);
+// launch with programmatic dependence on the preceding kernel, and a cluster along x
+cudaError_t launch_pdl(const void* kernel, dim3 grid, dim3 block, int smem, int cluster, cudaStream_t stream,
+                       void** args);
+// tensor map of a row-major byte matrix [rows][cols] with 128-byte swizzle and
+// a box of 128 columns x `box_rows` rows
+bool byte_map(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols, uint32_t box_rows);
+
+}  // namespace fp8
+}  // namespace sharq

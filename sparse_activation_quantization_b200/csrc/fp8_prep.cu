@@ -1,0 +1,362 @@
+// fp8_prep.cu - activations and weights to E4M3 with float32 block scales.
+//
+// Per row and 128 columns:  s = max|v| / 448,  code = e4m3(v * f32(1/s)),
+// where v is the row's RMS norm, its SwiGLU product or the row itself.
+// Everything is bound by HBM: each input is read once into registers, the
+// statistics are taken there and codes, scales and the new residual stream
+// are written once.
+#include "fp8.cuh"
+
+namespace sharq {
+namespace fp8 {
+
+namespace {
+
+enum { kPlain = 0, kResidual = 1, kSwiglu = 2 };
+
+struct PrepArgs {
+  const __nv_bfloat16* x;    // plain / residual: the input; SwiGLU: the gate
+  const __nv_bfloat16* b;    // residual: the stream; SwiGLU: up
+  __nv_bfloat16* h;          // residual: the new stream, or nullptr
+  const __nv_bfloat16* gamma;
+  uint8_t* codes;
+  float* scales;
+  long long ldx, ldb, ldh;
+  int T, K, lds;
+  float eps;
+};
+
+// v of 8 consecutive columns before the norm; the residual form returns the
+// bf16-rounded sum and stores it
+template <int kKind>
+__device__ __forceinline__ void load8(const PrepArgs& a, int t, int c, float (&v)[8]) {
+  unpack_bf16x8(*reinterpret_cast<const uint4*>(a.x + (size_t)t * a.ldx + c), v);
+  if (kKind == kPlain) return;
+  float w[8];
+  unpack_bf16x8(*reinterpret_cast<const uint4*>(a.b + (size_t)t * a.ldb + c), w);
+  if (kKind == kResidual) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] += w[i];
+    const uint4 h = pack_bf16x8(v);
+    if (a.h) *reinterpret_cast<uint4*>(a.h + (size_t)t * a.ldh + c) = h;
+    unpack_bf16x8(h, v);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = silu_mul(v[i], w[i]);
+  }
+}
+
+// scale and codes of one 128-block that 16 neighbouring lanes hold, 8 values
+// each; lanes past the row's end hold zeros and store nothing
+__device__ __forceinline__ void quant8(const PrepArgs& a, int t, int c, const float (&v)[8]) {
+  float m = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(v[i]));
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  const float s = block_scale_e4m3(m);
+  const float inv = __frcp_rn(s);
+  if (c < a.K) {
+    uint2 q;
+    q.x = e4m3x4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv);
+    q.y = e4m3x4(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv);
+    *reinterpret_cast<uint2*>(a.codes + (size_t)t * a.K + c) = q;
+    if ((c & (kBlock - 1)) == 0) a.scales[(size_t)(c / kBlock) * a.lds + t] = s;
+  }
+}
+
+// Without a norm every 128-block stands alone: half a warp per block.
+template <int kKind>
+__global__ void __launch_bounds__(256) fp8_quant_kernel(const PrepArgs a) {
+  pdl_trigger();
+  pdl_wait();
+  const int kb = blocks_of(a.K);
+  const long long total = (long long)a.T * kb;
+  const long long stride = (long long)gridDim.x * 16;
+  // the loop is uniform over the warp: both halves take part in the shuffles
+  for (long long i0 = (long long)blockIdx.x * 16 + (threadIdx.x >> 5) * 2; i0 < total; i0 += stride) {
+    const long long i = i0 + ((threadIdx.x >> 4) & 1);
+    const bool in = i < total;
+    const int t = in ? (int)(i / kb) : 0;
+    const int c = in ? (int)(i - (long long)t * kb) * kBlock + (threadIdx.x & 15) * 8 : a.K;
+    float v[8] = {};
+    if (c < a.K) load8<kKind>(a, t, c, v);
+    quant8(a, t, c, v);
+  }
+}
+
+// A row whose sum of squares float32 does not hold (an overflow, or squares
+// below its smallest normal value) takes its 1/rms in float64.
+__device__ __forceinline__ bool square_sum_fits(float ss) { return ss < 1e37f && ss > 1e-30f; }
+
+template <bool kWarpRow>
+__device__ __noinline__ double inv_rms_wide(double s2, const PrepArgs& a) {
+  __shared__ double part[32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s2 += __shfl_xor_sync(0xffffffffu, s2, o);
+  if (!kWarpRow) {
+    if (lane == 0) part[warp] = s2;
+    __syncthreads();
+    s2 = 0.0;
+    for (int w = 0; w < (int)(blockDim.x >> 5); ++w) s2 += part[w];
+  }
+  return 1.0 / sqrt(s2 / (double)a.K + (double)a.eps);
+}
+
+// With a norm, one CTA (or one warp) holds a row: R vectors of 8 columns per
+// thread.  kWarpRow: a warp per row, no barrier.
+template <int kKind, int R, bool kWarpRow>
+__global__ void __launch_bounds__(1024) fp8_norm_kernel(const PrepArgs a) {
+  __shared__ float part[32];
+  pdl_trigger();
+  pdl_wait();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int nthr = kWarpRow ? 32 : (int)blockDim.x;
+  const int me = kWarpRow ? lane : (int)threadIdx.x;
+  const int t = kWarpRow ? (int)(blockIdx.x * (blockDim.x >> 5)) + warp : (int)blockIdx.x;
+  if (kWarpRow && t >= a.T) return;
+  float v[R][8];
+  float ss = 0.0f;
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const int c = (r * nthr + me) * 8;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[r][i] = 0.0f;
+    if (c < a.K) load8<kKind>(a, t, c, v[r]);
+  }
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) ss = fmaf(v[r][i], v[r][i], ss);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+  if (!kWarpRow) {
+    if (lane == 0) part[warp] = ss;
+    __syncthreads();
+    ss = lane < (nthr >> 5) ? part[lane] : 0.0f;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+  }
+  const float inv = __frsqrt_rn(__fadd_rn(__fdiv_rn(ss, (float)a.K), a.eps));
+  if (!square_sum_fits(ss)) {  // the same for every thread of the row
+    double s2 = 0.0;
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s2 += (double)v[r][i] * (double)v[r][i];
+    const double inv2 = inv_rms_wide<kWarpRow>(s2, a);
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[r][i] = (float)((double)v[r][i] * inv2);
+  } else {
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[r][i] *= inv;
+  }
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const int c = (r * nthr + me) * 8;
+    if (c < a.K) {
+      float g[8];
+      unpack_bf16x8(*reinterpret_cast<const uint4*>(a.gamma + c), g);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[r][i] *= g[i];
+    }
+    quant8(a, t, c, v[r]);
+  }
+}
+
+// Rows longer than the registers of one CTA hold: the row is read twice.  The
+// second pass reads the stored sum where there is one (the first pass may have
+// overwritten the stream it was formed from).
+template <int kKind>
+__device__ __forceinline__ void reload8(const PrepArgs& a, int t, int c, float (&v)[8]) {
+  if (kKind == kResidual && a.h)
+    unpack_bf16x8(*reinterpret_cast<const uint4*>(a.h + (size_t)t * a.ldh + c), v);  // this thread's own store
+  else
+    load8<kKind>(a, t, c, v);
+}
+template <int kKind>
+__global__ void __launch_bounds__(1024) fp8_norm_long_kernel(const PrepArgs a) {
+  __shared__ float part[32];
+  pdl_trigger();
+  pdl_wait();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, t = blockIdx.x;
+  float ss = 0.0f;
+  for (int c = threadIdx.x * 8; c < a.K; c += 8192) {
+    float v[8];
+    load8<kKind>(a, t, c, v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) ss = fmaf(v[i], v[i], ss);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+  if (lane == 0) part[warp] = ss;
+  __syncthreads();
+  ss = part[lane];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+  double inv = (double)__frsqrt_rn(__fadd_rn(__fdiv_rn(ss, (float)a.K), a.eps));
+  const bool fits = square_sum_fits(ss);
+  if (!fits) {
+    double s2 = 0.0;
+    for (int c = threadIdx.x * 8; c < a.K; c += 8192) {
+      float v[8];
+      reload8<kKind>(a, t, c, v);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s2 += (double)v[i] * (double)v[i];
+    }
+    inv = inv_rms_wide<false>(s2, a);
+  }
+  for (int c0 = 0; c0 < a.K; c0 += 8192) {
+    const int c = c0 + threadIdx.x * 8;
+    float v[8] = {};
+    if (c < a.K) {
+      reload8<kKind>(a, t, c, v);
+      float g[8];
+      unpack_bf16x8(*reinterpret_cast<const uint4*>(a.gamma + c), g);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = (fits ? v[i] * (float)inv : (float)((double)v[i] * inv)) * g[i];
+    }
+    quant8(a, t, c, v);
+  }
+}
+
+template <int kKind, int R, bool kWarpRow>
+cudaError_t launch_norm(PrepArgs& a, int grid, int block, cudaStream_t stream) {
+  void* args[] = {&a};
+  return launch_pdl((const void*)fp8_norm_kernel<kKind, R, kWarpRow>, dim3(grid), dim3(block), 0, 1, stream, args);
+}
+
+template <int kKind>
+cudaError_t launch_kind(PrepArgs& a, cudaStream_t stream) {
+  void* args[] = {&a};
+  if (!a.gamma) {
+    const Device* d = device();
+    if (!d) return cudaErrorInvalidDevice;
+    const long long want = ((long long)a.T * blocks_of(a.K) + 15) / 16;
+    const long long most = (long long)d->sms * 8;
+    return launch_pdl((const void*)fp8_quant_kernel<kKind>, dim3((unsigned)(want < most ? want : most)), dim3(256), 0,
+                      1, stream, args);
+  }
+  if (a.K <= 1024) {
+    const int rows = 4;
+    const int grid = (a.T + rows - 1) / rows;
+    if (a.K <= 256) return launch_norm<kKind, 1, true>(a, grid, 32 * rows, stream);
+    if (a.K <= 512) return launch_norm<kKind, 2, true>(a, grid, 32 * rows, stream);
+    return launch_norm<kKind, 4, true>(a, grid, 32 * rows, stream);
+  }
+  const int vecs = (a.K + 7) / 8;
+  auto block = [&](int r) { return ((vecs + r - 1) / r + 31) / 32 * 32; };
+  if (vecs <= 1024) return launch_norm<kKind, 1, false>(a, a.T, block(1), stream);
+  if (vecs <= 2048) return launch_norm<kKind, 2, false>(a, a.T, block(2), stream);
+  if (vecs <= 4096) return launch_norm<kKind, 4, false>(a, a.T, block(4), stream);
+  return launch_pdl((const void*)fp8_norm_long_kernel<kKind>, dim3(a.T), dim3(1024), 0, 1, stream, args);
+}
+
+// --------------------------------------------------------------- weights ---
+
+// One 128 x 128 block of W [K][D] per CTA: amax, then codes transposed to
+// [D][K] through shared memory.  Thread (o, kg) holds columns 8 o .. 8 o + 7 of
+// rows 8 kg .. 8 kg + 7.  Shared memory holds row d as 16 chunks of 8 k-bytes,
+// chunk kg at kg ^ (d / 8), so that neither side meets bank conflicts.
+template <bool kVec>
+__global__ void __launch_bounds__(256) fp8_pack_kernel(const __nv_bfloat16* W, int K, int D, uint8_t* codes,
+                                                       float* scales) {
+  __shared__ __align__(16) uint8_t tile[128 * 128];
+  __shared__ float part[8];
+  pdl_trigger();
+  pdl_wait();
+  const int kb = blockIdx.x, db = blockIdx.y;
+  const size_t e = blockIdx.z;
+  const int o = threadIdx.x & 15, kg = threadIdx.x >> 4;
+  const int d0 = db * 128 + o * 8, k0 = kb * 128 + kg * 8;
+  const __nv_bfloat16* src = W + (e * K + k0) * (size_t)D + d0;
+  float v[8][8];
+  float m = 0.0f;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[j][i] = 0.0f;
+    if (k0 + j < K) {
+      if (kVec) {
+        if (d0 < D) unpack_bf16x8(*reinterpret_cast<const uint4*>(src + (size_t)j * D), v[j]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (d0 + i < D) v[j][i] = __bfloat162float(src[(size_t)j * D + i]);
+      }
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(v[j][i]));
+#pragma unroll
+  for (int s = 16; s > 0; s >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, s));
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = m;
+  __syncthreads();
+  m = part[0];
+#pragma unroll
+  for (int w = 1; w < 8; ++w) m = fmaxf(m, part[w]);
+  const float s = block_scale_e4m3(m);
+  const float inv = __frcp_rn(s);
+  if (threadIdx.x == 0) scales[(e * gridDim.y + db) * gridDim.x + kb] = s;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    uint2 q;
+    q.x = e4m3x4(v[0][i] * inv, v[1][i] * inv, v[2][i] * inv, v[3][i] * inv);
+    q.y = e4m3x4(v[4][i] * inv, v[5][i] * inv, v[6][i] * inv, v[7][i] * inv);
+    *reinterpret_cast<uint2*>(tile + (o * 8 + i) * 128 + ((kg ^ o) << 3)) = q;
+  }
+  __syncthreads();
+  const int q = threadIdx.x & 7;  // 16-byte chunk of the output row
+#pragma unroll
+  for (int it = 0; it < 4; ++it) {
+    const int r = it * 32 + (threadIdx.x >> 3);
+    const int ro = r >> 3;
+    uint4 w = *reinterpret_cast<const uint4*>(tile + r * 128 + (((2 * q) ^ (ro & ~1)) << 3));
+    if (ro & 1) w = make_uint4(w.z, w.w, w.x, w.y);
+    const int d = db * 128 + r, k = kb * 128 + q * 16;
+    if (d < D && k < K) *reinterpret_cast<uint4*>(codes + (e * D + d) * (size_t)K + k) = w;
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_prep(int kind, const void* x, long long ldx, const void* b, long long ldb, void* h, long long ldh,
+                        const void* gamma, float eps, int T, int K, uint8_t* codes, float* scales, int lds,
+                        cudaStream_t stream) {
+  if (T == 0) return cudaSuccess;
+  PrepArgs a;
+  a.x = static_cast<const __nv_bfloat16*>(x);
+  a.b = static_cast<const __nv_bfloat16*>(b);
+  a.h = static_cast<__nv_bfloat16*>(h);
+  a.gamma = static_cast<const __nv_bfloat16*>(gamma);
+  a.codes = codes;
+  a.scales = scales;
+  a.ldx = ldx;
+  a.ldb = ldb;
+  a.ldh = ldh;
+  a.T = T;
+  a.K = K;
+  a.lds = lds;
+  a.eps = eps;
+  if (kind == kResidual) return launch_kind<kResidual>(a, stream);
+  if (kind == kSwiglu) return launch_kind<kSwiglu>(a, stream);
+  return launch_kind<kPlain>(a, stream);
+}
+
+cudaError_t launch_pack(const void* W, int K, int D, int E, uint8_t* codes, float* scales, cudaStream_t stream) {
+  const __nv_bfloat16* w = static_cast<const __nv_bfloat16*>(W);
+  void* args[] = {&w, &K, &D, &codes, &scales};
+  const bool vec = D % 8 == 0 && reinterpret_cast<uintptr_t>(W) % 16 == 0;
+  return launch_pdl(vec ? (const void*)fp8_pack_kernel<true> : (const void*)fp8_pack_kernel<false>,
+                    dim3(blocks_of(K), blocks_of(D), E), dim3(256), 0, 1, stream, args);
+}
+
+}  // namespace fp8
+}  // namespace sharq
