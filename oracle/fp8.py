@@ -102,30 +102,35 @@ def route(logits, topk, renormalize=True):
 
 def moe(x, logits, w13, w2, topk, renormalize=True):
     """x [T, H]; w13 [E, 2 I, H] and w2 [E, H, I] dequantized.  Returns y, ids,
-    p and `size`: sum_j p sum_i |w2| (the size of what enters h's own error),
-    as needed for error bounds."""
+    p and a bound of a float32 evaluation's error per output:
+      - x as two E4M3 terms, the block's largest scaled to [128, 256): exact, or
+        off by half the spacing of the second term's smallest numbers, 2^-10
+        2^-4 of the scaled value = 2^-21 of the block's largest (at least 2^-107)
+      - h as three terms: 2^-12 of itself, or 2^-10 2^-8 = 2^-25 of the largest
+      - float32 sums of 128 products a block and then over blocks and terms"""
     x = np.asarray(x, np.float64)
     T, H = x.shape
     inner = w2.shape[-1]
     ids, p = route(logits, topk, renormalize)
     y = np.zeros((T, H))
     bound = np.zeros((T, H))
-    nkb = blocks(H)
+
+    def block_max(v):
+        pad = np.zeros(blocks(v.size) * BLOCK)
+        pad[:v.size] = np.abs(v)
+        return expand(np.maximum(pad.reshape(-1, BLOCK).max(-1), 2.0 ** -107), v.size, 0)
+
     for t in range(T):
+        dx = 2.0 ** -21 * block_max(x[t])
         for j in range(topk):
             e = ids[t, j]
             gu = w13[e] @ x[t]
-            mag = np.abs(w13[e]) @ np.abs(x[t])
+            a13, a2 = np.abs(w13[e]), np.abs(w2[e])
             g, u = gu[:inner], gu[inner:]
             h = silu(g) * u
-            # float32 sums of 128 products per block, then over blocks, K split eight ways
-            d = (128 + nkb + 16) * 2.0 ** -23 * mag
+            d = (2 * 128 + blocks(H) + 16) * 2.0 ** -23 * (a13 @ np.abs(x[t])) + a13 @ dx
             dh = 1.1 * np.abs(u) * d[:inner] + np.abs(silu(g)) * d[inner:] + 2.0 ** -16 * np.abs(h)
-            hb = np.zeros(blocks(inner) * BLOCK)
-            hb[:inner] = np.abs(h)
-            # h to f16 in a block whose largest value is scaled to [2^14, 2^15)
-            dh = dh + 2.0 ** -11 * np.abs(h) + 2.0 ** -38 * expand(hb.reshape(-1, BLOCK).max(-1), inner, 0)
-            a2 = np.abs(w2[e])
+            dh = dh + 2.0 ** -12 * np.abs(h) + 2.0 ** -25 * block_max(h)
             y[t] += p[t, j] * (w2[e] @ h)
-            bound[t] += p[t, j] * (a2 @ dh + (128 + blocks(inner) + topk + 16) * 2.0 ** -23 * (a2 @ np.abs(h)))
+            bound[t] += p[t, j] * (a2 @ dh + (3 * 128 + blocks(inner) + topk + 16) * 2.0 ** -23 * (a2 @ np.abs(h)))
     return y, ids, p, bound

@@ -13,7 +13,7 @@
 //           tiles alone cannot fill the SMs.
 //   pair    256 x 256 output tiles on CTA pairs (tcgen05 cta_group::2), a
 //           persistent grid.
-#include "fp8.cuh"
+#include "fp8_stream.cuh"
 
 namespace sharq {
 namespace fp8 {
@@ -39,84 +39,121 @@ __device__ __forceinline__ void mbar_arrive_cta(uint64_t* bar) {
 }
 
 // ------------------------------------------------------------ stream form ---
+// Item = 16 weight rows; the CTA's eight warps share its K block by block and
+// join their sums through shared memory.  A ring slot holds a unit of the
+// weight, the same 128 k of the NT x 8 rows of X, and both scales.
 
 constexpr int kStreamWarps = 8;
-constexpr int kStreamUnroll = 4;  // 128-k blocks whose loads are in flight per warp
+template <int NT>
+struct Stream {
+  static constexpr int kRing = NT == 1 ? 4 : 3;
+  static constexpr int kX = kWeightUnit, kXs = kX + 1024 * NT, kWs = kXs + 32 * NT;
+  static constexpr int kSlot = kWs + 16;
+  static constexpr int kSmemBytes = kStreamWarps * kRing * kSlot;
+};
 
 template <int NT>
-__global__ void __launch_bounds__(32 * kStreamWarps) fp8_stream_kernel(const LinearArgs a) {
-  __shared__ float red[kStreamWarps][16][8 * NT + 1];
+__global__ void __launch_bounds__(32 * kStreamWarps, 2) fp8_stream_kernel(const LinearArgs a) {
+  using C = Stream<NT>;
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ float red[2][kStreamWarps][16][8 * NT + 1];
   pdl_trigger();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, q = lane & 3;
-  const int d0 = blockIdx.x * 16;
-  const int nkb = blocks_of(a.K);
-  // rows past the last one read the last one and are not stored
-  const uint8_t* w0 = a.w + (size_t)min(d0 + g, a.D - 1) * a.K + 16 * q;
-  const uint8_t* w1 = a.w + (size_t)min(d0 + g + 8, a.D - 1) * a.K + 16 * q;
-  const float* ws = a.ws + (size_t)(d0 / kBlock) * nkb;
-  float acc[NT][4] = {};
-  pdl_wait();
-  for (int b0 = warp; b0 < nkb; b0 += kStreamWarps * kStreamUnroll) {
-    uint4 w[kStreamUnroll][2][2];
-#pragma unroll
-    for (int u = 0; u < kStreamUnroll; ++u) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int k = (b0 + u * kStreamWarps) * kBlock + 64 * h;
-        const bool in = k + 16 * q < a.K;
-        w[u][h][0] = in ? ld_stream(w0 + k) : make_uint4(0u, 0u, 0u, 0u);
-        w[u][h][1] = in ? ld_stream(w1 + k) : make_uint4(0u, 0u, 0u, 0u);
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < kStreamUnroll; ++u) {
-      const int b = b0 + u * kStreamWarps;
-      if (b >= nkb) break;
-      const float sw = ws[b];
+  const int nkb = blocks_of(a.K), items = (a.D + 15) / 16;
+  const uint32_t ring = smem_u32(smem) + warp * C::kRing * C::kSlot;
+  // the next unit to load
+  int li = blockIdx.x, lb = warp;
+  const uint8_t *w0 = nullptr, *w1 = nullptr;
+  const float* ws = nullptr;
+  auto item = [&]() {
+    const int d = li * 16 + g;  // rows past the last one read the last one and are not stored
+    w0 = a.w + (size_t)min(d, a.D - 1) * a.K + 16 * q;
+    w1 = a.w + (size_t)min(d + 8, a.D - 1) * a.K + 16 * q;
+    ws = a.ws + (size_t)(li / 8) * nkb;
+  };
+  auto load = [&](uint32_t slot) {
+    if (li < items && lb < nkb) {
+      const int k = lb * kBlock, left = a.K - k - 16 * q;
+      rows16_load(slot, w0 + k, w1 + k, left, lane);
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
         const int t = 8 * n + g;
+        const bool in = t < a.T;
+        const uint8_t* x = a.x + (size_t)(in ? t : 0) * a.K + k + 16 * q;
+        const uint32_t d = slot + C::kX + n * 1024 + lane * 16;
+        copy16(d, left > 0 ? x : a.x, in && left > 0 ? 16u : 0u);
+        copy16(d + 512, left > 64 ? x + 64 : a.x, in && left > 64 ? 16u : 0u);
+      }
+      if (lane < 2 * NT) {
+        const int n = min(4, a.T - 4 * lane);
+        copy16(slot + C::kXs + lane * 16, a.xs + (size_t)lb * a.lds + (n > 0 ? 4 * lane : 0), n > 0 ? 4u * n : 0u);
+      } else if (lane == 2 * NT) {
+        copy4(slot + C::kWs, ws + lb);
+      }
+      lb += kStreamWarps;
+      if (lb >= nkb) {
+        lb = warp;
+        li += gridDim.x;
+        if (li < items) item();
+      }
+    }
+    copies_commit();
+  };
+  pdl_wait();
+  item();
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int k = b * kBlock + 64 * h + 16 * q;
-          uint4 x = make_uint4(0u, 0u, 0u, 0u);
-          if (t < a.T && k < a.K) x = *reinterpret_cast<const uint4*>(a.x + (size_t)t * a.K + k);
-          mma_e4m3(c, w[u][h][0].x, w[u][h][1].x, w[u][h][0].y, w[u][h][1].y, x.x, x.y);
-          mma_e4m3(c, w[u][h][0].z, w[u][h][1].z, w[u][h][0].w, w[u][h][1].w, x.z, x.w);
-        }
-        const int tc = 8 * n + 2 * q;  // the accumulator's columns are tokens tc, tc + 1
-        const float s0 = tc < a.T ? a.xs[(size_t)b * a.lds + tc] * sw : 0.0f;
-        const float s1 = tc + 1 < a.T ? a.xs[(size_t)b * a.lds + tc + 1] * sw : 0.0f;
-        acc[n][0] = fmaf(c[0], s0, acc[n][0]);
-        acc[n][1] = fmaf(c[1], s1, acc[n][1]);
-        acc[n][2] = fmaf(c[2], s0, acc[n][2]);
-        acc[n][3] = fmaf(c[3], s1, acc[n][3]);
+  for (int i = 0; i < C::kRing; ++i) load(ring + i * C::kSlot);
+  uint32_t slot = ring;
+  int buf = 0;
+  for (int it = blockIdx.x; it < items; it += gridDim.x, buf ^= 1) {
+    float acc[NT][4] = {};
+    for (int b = warp; b < nkb; b += kStreamWarps) {
+      copies_wait<C::kRing - 1>();
+      __syncwarp();  // the scales come from other lanes' copies
+      WeightUnit w;
+      w.read(slot, lane);
+      float s_w;
+      asm volatile("ld.shared.f32 %0, [%1];" : "=f"(s_w) : "r"(slot + C::kWs) : "memory");
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const uint32_t x = slot + C::kX + n * 1024 + lane * 16;
+        float c[4];
+        w.times(lds128(x), lds128(x + 512), c);
+        const float2 s = lds_f2(slot + C::kXs + (8 * n + 2 * q) * 4);
+        acc[n][0] = fmaf(c[0], s.x * s_w, acc[n][0]);
+        acc[n][1] = fmaf(c[1], s.y * s_w, acc[n][1]);
+        acc[n][2] = fmaf(c[2], s.x * s_w, acc[n][2]);
+        acc[n][3] = fmaf(c[3], s.y * s_w, acc[n][3]);
+      }
+      __syncwarp();
+      load(slot);
+      slot = slot == ring + (C::kRing - 1) * C::kSlot ? ring : slot + C::kSlot;
+    }
+    auto& r = red[buf];  // two in turn: an item's readers are past it before the next but one writes it
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      r[warp][g][8 * n + 2 * q] = acc[n][0];
+      r[warp][g][8 * n + 2 * q + 1] = acc[n][1];
+      r[warp][g + 8][8 * n + 2 * q] = acc[n][2];
+      r[warp][g + 8][8 * n + 2 * q + 1] = acc[n][3];
+    }
+    __syncthreads();
+    if (threadIdx.x < 128 * NT) {
+      const int t = threadIdx.x >> 4, d = threadIdx.x & 15;
+      float s = r[0][d][t];
+#pragma unroll
+      for (int v = 1; v < kStreamWarps; ++v) s += r[v][d][t];
+      if (t < a.T && it * 16 + d < a.D) {
+        const size_t o = (size_t)t * a.ldy + it * 16 + d;
+        if (a.out_f32)
+          static_cast<float*>(a.y)[o] = s;
+        else
+          static_cast<__nv_bfloat16*>(a.y)[o] = __float2bfloat16_rn(s);
       }
     }
   }
-#pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    red[warp][g][8 * n + 2 * q] = acc[n][0];
-    red[warp][g][8 * n + 2 * q + 1] = acc[n][1];
-    red[warp][g + 8][8 * n + 2 * q] = acc[n][2];
-    red[warp][g + 8][8 * n + 2 * q + 1] = acc[n][3];
-  }
-  __syncthreads();
-  for (int i = threadIdx.x; i < 128 * NT; i += 32 * kStreamWarps) {
-    const int t = i >> 4, r = i & 15;
-    float s = red[0][r][t];
-#pragma unroll
-    for (int v = 1; v < kStreamWarps; ++v) s += red[v][r][t];
-    if (t < a.T && d0 + r < a.D) {
-      const size_t o = (size_t)t * a.ldy + d0 + r;
-      if (a.out_f32)
-        static_cast<float*>(a.y)[o] = s;
-      else
-        static_cast<__nv_bfloat16*>(a.y)[o] = __float2bfloat16_rn(s);
-    }
-  }
+  copies_wait<0>();
 }
 
 // -------------------------------------------------------------- tile form ---
@@ -628,9 +665,15 @@ cudaError_t launch_linear(const uint8_t* x, const float* xs, int lds, int T, int
   a.vec_y = reinterpret_cast<uintptr_t>(y) % 16 == 0 && (ldy * (out_f32 ? 4 : 2)) % 16 == 0;
   a.splits = 1;
   if (T <= 16) {
+    static bool done1[64] = {}, done2[64] = {};
+    const bool one = T <= 8;
+    const void* k = one ? (const void*)fp8_stream_kernel<1> : (const void*)fp8_stream_kernel<2>;
+    const int smem = one ? Stream<1>::kSmemBytes : Stream<2>::kSmemBytes;
+    cudaError_t e = opt_in_smem(k, smem, one ? done1 : done2);
+    if (e != cudaSuccess) return e;
     void* args[] = {&a};
-    return launch_pdl(T <= 8 ? (const void*)fp8_stream_kernel<1> : (const void*)fp8_stream_kernel<2>,
-                      dim3((D + 15) / 16), dim3(32 * kStreamWarps), 0, 1, stream, args);
+    const int items = (D + 15) / 16, most = 2 * dev->sms;
+    return launch_pdl(k, dim3(items < most ? items : most), dim3(32 * kStreamWarps), smem, 1, stream, args);
   }
   CUtensorMap mx, mw;
   if (!byte_map(&mx, x, (uint64_t)T, (uint64_t)K, 128) || !byte_map(&mw, w, (uint64_t)D, (uint64_t)K, 128))
