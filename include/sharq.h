@@ -472,13 +472,15 @@ int sharq_fp8_linear(const sharq_fp8_act *a, const sharq_fp8_weight *w, void *d_
  *   y[t] = sum_j p(t, j) W2_e (silu(Wg_e x_t) * (Wu_e x_t)),  e = chosen(t)[j]
  * w13: E experts of D = 2 I rows, the gate's I rows and then the up's, K = H;
  * w2: E experts of D = H, K = I.  d_X: bf16 [T][H], row stride ldx; activations
- * are not quantized.  h is float32 and multiplied as f16 with a power-of-two
- * scale per 128 (2^-11 relative).  d_Y: bf16 [T][H], row stride ldy; it may be
- * d_X.  d_topk_ids (int32) and d_topk_weights (float32), [T][topk]: written
+ * are not quantized: x enters as two E4M3 terms of a power-of-two scale per 128
+ * (exact down to 2^-13 of the block's largest), h (float32) as three (2^-12
+ * relative).  An expert of weight 0 is not evaluated, so a masked token's x may
+ * hold anything.  d_Y: bf16 [T][H], row stride ldy; it may be d_X.  d_topk_ids (int32) and d_topk_weights (float32), [T][topk]: written
  * unless NULL.
  * T <= 64, topk <= 16 and <= E, E <= 512 (SHARQ_ERR_UNSUPPORTED_SHAPE).
- * d_ws: at least sharq_fp8_moe_workspace_bytes (no initial value); calls that
- * may run at the same time need one each.
+ * d_ws: at least sharq_fp8_moe_workspace_bytes, zeroed once before its first use
+ * (its first word is the error word of sharq_check_status); calls that may run
+ * at the same time need one each.
  */
 #define SHARQ_FP8_MOE_MAX_T 64
 #define SHARQ_FP8_MOE_MAX_TOPK 16

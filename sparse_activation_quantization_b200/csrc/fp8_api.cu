@@ -68,7 +68,10 @@ cudaError_t launch_pdl(const void* kernel, dim3 grid, dim3 block, int smem, int 
   return cudaLaunchKernelExC(&cfg, kernel, args);
 }
 
-bool byte_map(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols, uint32_t box_rows) {
+namespace {
+// tensor map of bytes, 128-byte swizzle; dims, strides (of all but the first axis) and box innermost first
+bool tensor_map(CUtensorMap* map, const void* base, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
+                const cuuint32_t* box) {
   using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                               const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                               CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
@@ -82,13 +85,23 @@ bool byte_map(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols, 
       return false;
     encode = reinterpret_cast<Encode>(f);
   }
-  const cuuint64_t dims[2] = {cols, rows};
-  const cuuint64_t strides[1] = {cols};
-  const cuuint32_t box[2] = {128, box_rows};
-  const cuuint32_t elem[2] = {1, 1};
-  return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, elem,
+  const cuuint32_t elem[4] = {1, 1, 1, 1};
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, (cuuint32_t)rank, const_cast<void*>(base), dims, strides, box, elem,
                 CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+}  // namespace
+
+bool byte_map(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols, uint32_t box_rows) {
+  const cuuint64_t dims[2] = {cols, rows}, strides[1] = {cols};
+  const cuuint32_t box[2] = {128, box_rows};
+  return tensor_map(map, base, 2, dims, strides, box);
+}
+
+bool halves_map(CUtensorMap* map, const void* base, uint64_t E, uint64_t rows, uint64_t cols, uint32_t box_rows) {
+  const cuuint64_t dims[4] = {cols, rows, 2, E}, strides[3] = {cols, rows * cols, 2 * rows * cols};
+  const cuuint32_t box[4] = {128, box_rows, 2, 1};
+  return tensor_map(map, base, 4, dims, strides, box);
 }
 
 }  // namespace fp8

@@ -5,15 +5,14 @@
 //
 // The tensor cores sum the products of one 128-k block exactly as they are;
 // each block's sum is then scaled and added in float32 registers.  Three
-// kernels, chosen by shape (fp8_linear_plan):
-//   stream  few rows: every weight byte goes from HBM to a register once and
-//           into warp-level MMAs (m16n8k32), 16 weight rows per CTA, K split
-//           over its warps.
+// kernels, chosen by shape (launch_linear):
+//   skinny  up to 64 rows: 128 weight rows are the MMA's M and the rows of X its
+//           N (fp8_skinny.cuh), K split over a cluster.
 //   tile    128 x 128 output tiles on tcgen05, K split over a cluster when the
 //           tiles alone cannot fill the SMs.
 //   pair    256 x 256 output tiles on CTA pairs (tcgen05 cta_group::2), a
 //           persistent grid.
-#include "fp8_stream.cuh"
+#include "fp8_skinny.cuh"
 
 namespace sharq {
 namespace fp8 {
@@ -34,126 +33,220 @@ struct LinearArgs {
   int splits;
 };
 
-__device__ __forceinline__ void mbar_arrive_cta(uint64_t* bar) {
-  asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
-}
-
-// ------------------------------------------------------------ stream form ---
-// Item = 16 weight rows; the CTA's eight warps share its K block by block and
-// join their sums through shared memory.  A ring slot holds a unit of the
-// weight, the same 128 k of the NT x 8 rows of X, and both scales.
-
-constexpr int kStreamWarps = 8;
-template <int NT>
-struct Stream {
-  static constexpr int kRing = NT == 1 ? 4 : 3;
-  static constexpr int kX = kWeightUnit, kXs = kX + 1024 * NT, kWs = kXs + 32 * NT;
-  static constexpr int kSlot = kWs + 16;
-  static constexpr int kSmemBytes = kStreamWarps * kRing * kSlot;
-};
-
-template <int NT>
-__global__ void __launch_bounds__(32 * kStreamWarps, 2) fp8_stream_kernel(const LinearArgs a) {
-  using C = Stream<NT>;
-  extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ float red[2][kStreamWarps][16][8 * NT + 1];
-  pdl_trigger();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int g = lane >> 2, q = lane & 3;
-  const int nkb = blocks_of(a.K), items = (a.D + 15) / 16;
-  const uint32_t ring = smem_u32(smem) + warp * C::kRing * C::kSlot;
-  // the next unit to load
-  int li = blockIdx.x, lb = warp;
-  const uint8_t *w0 = nullptr, *w1 = nullptr;
-  const float* ws = nullptr;
-  auto item = [&]() {
-    const int d = li * 16 + g;  // rows past the last one read the last one and are not stored
-    w0 = a.w + (size_t)min(d, a.D - 1) * a.K + 16 * q;
-    w1 = a.w + (size_t)min(d + 8, a.D - 1) * a.K + 16 * q;
-    ws = a.ws + (size_t)(li / 8) * nkb;
-  };
-  auto load = [&](uint32_t slot) {
-    if (li < items && lb < nkb) {
-      const int k = lb * kBlock, left = a.K - k - 16 * q;
-      rows16_load(slot, w0 + k, w1 + k, left, lane);
+// four consecutive columns of a row
+__device__ __forceinline__ void store_cols4(const LinearArgs& a, int row, int col, float4 v) {
+  const size_t o = (size_t)row * a.ldy + col;
+  if (a.out_f32) {
+    float* y = static_cast<float*>(a.y) + o;
+    if (a.vec_y && col + 4 <= a.D) {
+      *reinterpret_cast<float4*>(y) = v;
+    } else {
+      const float e[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        const int t = 8 * n + g;
-        const bool in = t < a.T;
-        const uint8_t* x = a.x + (size_t)(in ? t : 0) * a.K + k + 16 * q;
-        const uint32_t d = slot + C::kX + n * 1024 + lane * 16;
-        copy16(d, left > 0 ? x : a.x, in && left > 0 ? 16u : 0u);
-        copy16(d + 512, left > 64 ? x + 64 : a.x, in && left > 64 ? 16u : 0u);
-      }
-      if (lane < 2 * NT) {
-        const int n = min(4, a.T - 4 * lane);
-        copy16(slot + C::kXs + lane * 16, a.xs + (size_t)lb * a.lds + (n > 0 ? 4 * lane : 0), n > 0 ? 4u * n : 0u);
-      } else if (lane == 2 * NT) {
-        copy4(slot + C::kWs, ws + lb);
-      }
-      lb += kStreamWarps;
-      if (lb >= nkb) {
-        lb = warp;
-        li += gridDim.x;
-        if (li < items) item();
-      }
+      for (int i = 0; i < 4; ++i)
+        if (col + i < a.D) y[i] = e[i];
     }
-    copies_commit();
-  };
-  pdl_wait();
-  item();
+  } else {
+    __nv_bfloat16* y = static_cast<__nv_bfloat16*>(a.y) + o;
+    if (a.vec_y && col + 4 <= a.D) {
+      *reinterpret_cast<uint2*>(y) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+    } else {
+      const float e[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-  for (int i = 0; i < C::kRing; ++i) load(ring + i * C::kSlot);
-  uint32_t slot = ring;
-  int buf = 0;
-  for (int it = blockIdx.x; it < items; it += gridDim.x, buf ^= 1) {
-    float acc[NT][4] = {};
-    for (int b = warp; b < nkb; b += kStreamWarps) {
-      copies_wait<C::kRing - 1>();
-      __syncwarp();  // the scales come from other lanes' copies
-      WeightUnit w;
-      w.read(slot, lane);
-      float s_w;
-      asm volatile("ld.shared.f32 %0, [%1];" : "=f"(s_w) : "r"(slot + C::kWs) : "memory");
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        const uint32_t x = slot + C::kX + n * 1024 + lane * 16;
-        float c[4];
-        w.times(lds128(x), lds128(x + 512), c);
-        const float2 s = lds_f2(slot + C::kXs + (8 * n + 2 * q) * 4);
-        acc[n][0] = fmaf(c[0], s.x * s_w, acc[n][0]);
-        acc[n][1] = fmaf(c[1], s.y * s_w, acc[n][1]);
-        acc[n][2] = fmaf(c[2], s.x * s_w, acc[n][2]);
-        acc[n][3] = fmaf(c[3], s.y * s_w, acc[n][3]);
-      }
-      __syncwarp();
-      load(slot);
-      slot = slot == ring + (C::kRing - 1) * C::kSlot ? ring : slot + C::kSlot;
-    }
-    auto& r = red[buf];  // two in turn: an item's readers are past it before the next but one writes it
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      r[warp][g][8 * n + 2 * q] = acc[n][0];
-      r[warp][g][8 * n + 2 * q + 1] = acc[n][1];
-      r[warp][g + 8][8 * n + 2 * q] = acc[n][2];
-      r[warp][g + 8][8 * n + 2 * q + 1] = acc[n][3];
-    }
-    __syncthreads();
-    if (threadIdx.x < 128 * NT) {
-      const int t = threadIdx.x >> 4, d = threadIdx.x & 15;
-      float s = r[0][d][t];
-#pragma unroll
-      for (int v = 1; v < kStreamWarps; ++v) s += r[v][d][t];
-      if (t < a.T && it * 16 + d < a.D) {
-        const size_t o = (size_t)t * a.ldy + it * 16 + d;
-        if (a.out_f32)
-          static_cast<float*>(a.y)[o] = s;
-        else
-          static_cast<__nv_bfloat16*>(a.y)[o] = __float2bfloat16_rn(s);
-      }
+      for (int i = 0; i < 4; ++i)
+        if (col + i < a.D) y[i] = __float2bfloat16_rn(e[i]);
     }
   }
-  copies_wait<0>();
+}
+
+// ------------------------------------------------------------ skinny form ---
+// 128 weight rows per CTA (or per cluster of S CTAs that share its K) against
+// all rows of X at once, as fp8_skinny.cuh describes.
+//   warps 0-3  sums: a thread holds one weight row and every row of X
+//   warp 4     one thread copies: the weight's box, X's box and the rows'
+//              scales of the block
+//   warp 5     TMEM allocation; one thread issues the MMAs
+// Two CTAs reside on an SM, so one's start and end hide behind the other's
+// copies.  A cluster joins its partial sums in rank order over distributed
+// shared memory (the ring, free by then).
+
+template <int kN>
+struct Skinny {
+  static constexpr int kStages = kN == 16 ? 6 : (kN == 32 ? 5 : 4);
+  static constexpr int kStageBytes = kUnitBytes + kN * kBlock;
+  static constexpr int kThreads = 192;
+  static constexpr int kTmem = tmem_cols(kN * kStages);
+  static constexpr int kSmemBytes = kStages * kStageBytes + 1024;
+  static_assert(kN * kUnitRows * 4 <= kStages * kStageBytes, "the sums must fit the ring");
+  static_assert(2 * kTmem <= 512, "two CTAs share the SM's TMEM");
+};
+
+__device__ __forceinline__ void store_one(const LinearArgs& a, size_t o, float v) {
+  if (a.out_f32)
+    static_cast<float*>(a.y)[o] = v;
+  else
+    static_cast<__nv_bfloat16*>(a.y)[o] = __float2bfloat16_rn(v);
+}
+
+template <int kN>
+__global__ void __launch_bounds__(Skinny<kN>::kThreads, 2)
+    fp8_skinny_kernel(const __grid_constant__ CUtensorMap mapx, const __grid_constant__ CUtensorMap mapw,
+                      const LinearArgs a) {
+  using C = Skinny<kN>;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) SkinnyBars<C::kStages> bars;
+  __shared__ __align__(16) float xs_sh[C::kStages][kN];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int S = a.splits;
+  const int rank = S > 1 ? (int)cluster_ctarank() : 0;
+  const int first = (int)blockIdx.x / S, step = (int)gridDim.x / S;
+  const int tiles = (a.D + kUnitRows - 1) / kUnitRows, nkb = blocks_of(a.K);
+  const int b0 = (int)((long long)rank * nkb / S), b1 = (int)((long long)(rank + 1) * nkb / S);
+
+  if (threadIdx.x == 128) {
+    tma_prefetch_map(&mapx);
+    tma_prefetch_map(&mapw);
+    bars.init(1);
+    for (int i = 0; i < C::kStages && b0 + i < b1; ++i)
+      tma_prefetch_2d(&mapw, (b0 + i) * kBlock, first * kUnitRows);
+  }
+  if (warp == 5) {
+    tmem_alloc(&bars.tmem, C::kTmem);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  pdl_trigger();  // after the allocation: the next grid's CTAs wait for this one with TMEM in hand
+  pdl_wait();
+  const uint32_t tmem = bars.tmem;
+  const uint64_t deadline = globaltimer_ns() + kWaitNs;
+  float acc[kN];
+
+  if (warp == 4) {
+    if (elect_one()) {
+      // scales are read in whole 16-byte groups of a column, whose length is a multiple of 4
+      const uint32_t xs_bytes = (uint32_t)(a.T + 3) / 4 * 16;
+      RingPos<C::kStages> p;
+      int n = 0;
+      for (int tile = first; tile < tiles && !bars.abort; tile += step)
+        for (int b = b0; b < b1; ++b, ++n, p.next()) {
+          if (!wait_empty(bars, p, deadline)) {
+            bars.give_up(a.err);
+            break;
+          }
+          uint8_t* st = smem + p.s * C::kStageBytes;
+          mbar_arrive_expect_tx(&bars.full[p.s], C::kStageBytes + xs_bytes);
+          tma_2d(st, &mapw, b * kBlock, tile * kUnitRows, &bars.full[p.s]);
+          tma_2d(st + kUnitBytes, &mapx, b * kBlock, 0, &bars.full[p.s]);
+          bulk_g2s(xs_sh[p.s], a.xs + (size_t)b * a.lds, xs_bytes, &bars.full[p.s]);
+        }
+      if (bars.abort) drain_copies(bars, n);
+    }
+  } else if (warp == 5) {
+    if (elect_one()) {
+      RingPos<C::kStages> p;
+      for (int tile = first; tile < tiles && !bars.abort; tile += step)
+        for (int b = b0; b < b1; ++b, p.next()) {
+          if (!mbar_wait(&bars.full[p.s], p.phase, deadline, &bars.abort)) {
+            bars.give_up(a.err);
+            break;
+          }
+          tc_fence_after();
+          unit_mma(tmem + p.s * kN, smem_u32(smem + p.s * C::kStageBytes), idesc_e4m3(kUnitRows, kN));
+          tc_commit(&bars.done[p.s]);
+        }
+    }
+  } else {
+    RingPos<C::kStages> p;
+    for (int tile = first; tile < tiles && !bars.abort; tile += step) {
+      ScaleRow ws;
+      ws.start(a.ws + (size_t)tile * nkb, nkb, b0, lane);
+#pragma unroll
+      for (int n = 0; n < kN; ++n) acc[n] = 0.0f;
+      for (int b = b0; b < b1; ++b, p.next()) {
+        const float s_w = ws.at(b, lane);
+        if (!wait_done(bars, p, deadline)) {
+          bars.give_up(a.err);
+          break;
+        }
+        uint32_t v[kN];
+        tmem_read(tmem + ((uint32_t)(warp * 32) << 16) + p.s * kN, v);
+        tmem_ld_wait();
+#pragma unroll
+        for (int n = 0; n < kN; n += 4) {
+          const float4 x = *reinterpret_cast<const float4*>(&xs_sh[p.s][n]);
+          acc[n] = fmaf(__uint_as_float(v[n]), x.x * s_w, acc[n]);
+          acc[n + 1] = fmaf(__uint_as_float(v[n + 1]), x.y * s_w, acc[n + 1]);
+          acc[n + 2] = fmaf(__uint_as_float(v[n + 2]), x.z * s_w, acc[n + 2]);
+          acc[n + 3] = fmaf(__uint_as_float(v[n + 3]), x.w * s_w, acc[n + 3]);
+        }
+        release_unit(bars, p, lane);
+      }
+      const int d = tile * kUnitRows + threadIdx.x;
+      if (S == 1 && d < a.D && !bars.abort) {
+#pragma unroll
+        for (int n = 0; n < kN; ++n)
+          if (n < a.T) store_one(a, (size_t)n * a.ldy + d, acc[n]);
+      }
+    }
+    if (S > 1) {  // one tile per cluster; its last sums were read, so the ring is free
+      asm volatile("bar.sync 1, 128;" ::: "memory");
+      float* out = reinterpret_cast<float*>(smem);
+#pragma unroll
+      for (int n = 0; n < kN; ++n)
+        if (n < a.T) out[n * kUnitRows + threadIdx.x] = acc[n];
+    }
+  }
+  if (S > 1) {
+    cluster_sync_all();  // every partial tile is in its CTA's shared memory
+    const uint32_t base = smem_u32(smem);
+    const int total = a.T * (kUnitRows / 4);
+    const int i1 = (rank + 1) * total / S;
+    for (int i = rank * total / S + (int)threadIdx.x; i < i1 && !bars.abort; i += C::kThreads) {
+      float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      for (int p = 0; p < S; ++p) {
+        const float4 o = ld_shared_cluster_f4(mapa_shared(base + i * 16, (uint32_t)p));
+        v.x += o.x;
+        v.y += o.y;
+        v.z += o.z;
+        v.w += o.w;
+      }
+      store_cols4(a, i / (kUnitRows / 4), first * kUnitRows + i % (kUnitRows / 4) * 4, v);
+    }
+    cluster_sync_all();  // no CTA leaves while a peer reads its sums
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 5) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::kTmem);
+  }
+}
+
+template <int kN>
+cudaError_t launch_skinny(LinearArgs& a, const Device* dev, cudaStream_t stream) {
+  using C = Skinny<kN>;
+  CUtensorMap mx, mw;
+  if (!byte_map(&mx, a.x, (uint64_t)a.T, (uint64_t)a.K, kN) ||
+      !byte_map(&mw, a.w, (uint64_t)a.D, (uint64_t)a.K, kUnitRows))
+    return cudaErrorInvalidValue;
+  static bool done[64] = {};
+  cudaError_t e = opt_in_smem((const void*)fp8_skinny_kernel<kN>, C::kSmemBytes, done);
+  if (e != cudaSuccess) return e;
+  const int tiles = (a.D + kUnitRows - 1) / kUnitRows, most = 2 * dev->sms, nkb = blocks_of(a.K);
+  // A CTA per SM; a second one where each then still has 16 units or more.  Measured: 28 tiles of 148 blocks
+  // 15.8 us at one, 14.5 at two; 36 tiles of 28 blocks 6.5 and 9.9.
+  int s = most / tiles;
+  if (s > 8) s = 8;
+  if (s * tiles > dev->sms && nkb < 16 * s) s = dev->sms / tiles;
+  s = s < 1 ? 1 : s;
+  a.splits = s < nkb ? s : nkb;
+  void* args[] = {&mx, &mw, &a};
+  const int grid = a.splits > 1 ? tiles * a.splits : (tiles < most ? tiles : most);
+  return launch_pdl((const void*)fp8_skinny_kernel<kN>, dim3(grid), dim3(C::kThreads), C::kSmemBytes, a.splits, stream,
+                    args);
 }
 
 // -------------------------------------------------------------- tile form ---
@@ -182,32 +275,6 @@ struct Tile {
 
 __device__ __forceinline__ void consumer_barrier() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
-// one output value pair of four consecutive columns of a row
-__device__ __forceinline__ void store_cols4(const LinearArgs& a, int row, int col, float4 v) {
-  const size_t o = (size_t)row * a.ldy + col;
-  if (a.out_f32) {
-    float* y = static_cast<float*>(a.y) + o;
-    if (a.vec_y && col + 4 <= a.D) {
-      *reinterpret_cast<float4*>(y) = v;
-    } else {
-      const float e[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (col + i < a.D) y[i] = e[i];
-    }
-  } else {
-    __nv_bfloat16* y = static_cast<__nv_bfloat16*>(a.y) + o;
-    if (a.vec_y && col + 4 <= a.D) {
-      *reinterpret_cast<uint2*>(y) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
-    } else {
-      const float e[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (col + i < a.D) y[i] = __float2bfloat16_rn(e[i]);
-    }
-  }
-}
-
 __global__ void __launch_bounds__(Tile::kThreads, 1)
     fp8_tile_kernel(const __grid_constant__ CUtensorMap mapx, const __grid_constant__ CUtensorMap mapw,
                     const LinearArgs a) {
@@ -226,9 +293,7 @@ __global__ void __launch_bounds__(Tile::kThreads, 1)
   const int nt = blockIdx.y, mt = blockIdx.z;
   const int nkb = blocks_of(a.K);
   const int b0 = (int)((long long)rank * nkb / S), b1 = (int)((long long)(rank + 1) * nkb / S);
-  const uint64_t deadline = globaltimer_ns() + kWaitNs;
 
-  pdl_trigger();
   if (threadIdx.x == 0) {
     tma_prefetch_map(&mapx);
     tma_prefetch_map(&mapw);
@@ -251,10 +316,12 @@ __global__ void __launch_bounds__(Tile::kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_base_sh;
+  pdl_trigger();  // after the allocation: the next grid's CTAs wait for this one with TMEM in hand
   pdl_wait();
+  const uint64_t deadline = globaltimer_ns() + kWaitNs;
 
   if (warp == 0) {
-    if (lane == 0) {
+    if (elect_one()) {
       int i = 0;
       for (int b = b0; b < b1; ++b, ++i) {
         const int s = i % C::kStages;
@@ -276,7 +343,7 @@ __global__ void __launch_bounds__(Tile::kThreads, 1)
       }
     }
   } else if (warp == 1) {
-    if (lane == 0) {
+    if (elect_one()) {
       constexpr uint32_t idesc = idesc_e4m3(C::BM, C::BN);
       for (int b = b0, i = 0; b < b1; ++b, ++i) {
         const int s = i % C::kStages, u = i % C::kBufs;
@@ -308,7 +375,7 @@ __global__ void __launch_bounds__(Tile::kThreads, 1)
       const int u = i % C::kBufs;
       const float s = s_next;
       if (b + 1 < b1) s_next = xs[(size_t)(b + 1) * a.lds] * ws[b + 1];
-      if (!mbar_wait(&acc_full[u], (i / C::kBufs) & 1, deadline, &abort_sh)) {
+      if (!__all_sync(0xffffffffu, mbar_wait(&acc_full[u], (i / C::kBufs) & 1, deadline, &abort_sh))) {
         record_error_word(a.err, kErrTimeoutWord);
         abort_sh = 1;
         break;
@@ -470,7 +537,6 @@ __global__ void __launch_bounds__(Pair::kThreads, 1)
     }
   };
 
-  pdl_trigger();
   if (threadIdx.x == 0) {
     tma_prefetch_map(&mapx);
     tma_prefetch_map(&mapw);
@@ -494,11 +560,12 @@ __global__ void __launch_bounds__(Pair::kThreads, 1)
   cluster_sync_all();  // the peer's barriers and TMEM exist before any pair traffic
   tc_fence_after();
   const uint32_t tmem = tmem_base_sh;
+  pdl_trigger();  // after the allocation: the next grid's CTAs wait for this one with TMEM in hand
   pdl_wait();
 
   if (warp < 4) {
     regs_other();
-    if (warp == 0 && lane == 0) {
+    if (warp == 0 && elect_one()) {
       const uint32_t full_lead = mapa_shared(smem_u32(&full_bar[0]), 0);
       int i = 0;
       for (int tile = pair; tile < ntiles && !abort_sh; tile += npairs) {
@@ -525,7 +592,7 @@ __global__ void __launch_bounds__(Pair::kThreads, 1)
       for (int j = i > C::kStages ? i - C::kStages : 0; j < i; ++j)
         while (!mbar_try_wait_cluster(&empty_bar[j % C::kStages], (j / C::kStages) & 1) && globaltimer_ns() < lim) {
         }
-    } else if (warp == 1 && lane == 0 && leader) {
+    } else if (warp == 1 && leader && elect_one()) {
       constexpr uint32_t idesc = idesc_e4m3(C::BM, C::BN);
       int i = 0;
       for (int tile = pair; tile < ntiles && !abort_sh; tile += npairs) {
@@ -570,7 +637,7 @@ __global__ void __launch_bounds__(Pair::kThreads, 1)
         const int u = i % C::kBufs;
         const float s = s_next;
         if (b + 1 < nkb) s_next = xs[(size_t)(b + 1) * a.lds] * ws[b + 1];
-        if (!mbar_wait_cluster(&acc_full[u], (i / C::kBufs) & 1, deadline, &abort_sh)) {
+        if (!__all_sync(0xffffffffu, mbar_wait_cluster(&acc_full[u], (i / C::kBufs) & 1, deadline, &abort_sh))) {
           record_error_word(a.err, kErrTimeoutWord);
           abort_sh = 1;
           break;
@@ -664,17 +731,9 @@ cudaError_t launch_linear(const uint8_t* x, const float* xs, int lds, int T, int
   a.out_f32 = out_f32;
   a.vec_y = reinterpret_cast<uintptr_t>(y) % 16 == 0 && (ldy * (out_f32 ? 4 : 2)) % 16 == 0;
   a.splits = 1;
-  if (T <= 16) {
-    static bool done1[64] = {}, done2[64] = {};
-    const bool one = T <= 8;
-    const void* k = one ? (const void*)fp8_stream_kernel<1> : (const void*)fp8_stream_kernel<2>;
-    const int smem = one ? Stream<1>::kSmemBytes : Stream<2>::kSmemBytes;
-    cudaError_t e = opt_in_smem(k, smem, one ? done1 : done2);
-    if (e != cudaSuccess) return e;
-    void* args[] = {&a};
-    const int items = (D + 15) / 16, most = 2 * dev->sms;
-    return launch_pdl(k, dim3(items < most ? items : most), dim3(32 * kStreamWarps), smem, 1, stream, args);
-  }
+  if (T <= 16) return launch_skinny<16>(a, dev, stream);
+  if (T <= 32) return launch_skinny<32>(a, dev, stream);
+  if (T <= 64) return launch_skinny<64>(a, dev, stream);
   CUtensorMap mx, mw;
   if (!byte_map(&mx, x, (uint64_t)T, (uint64_t)K, 128) || !byte_map(&mw, w, (uint64_t)D, (uint64_t)K, 128))
     return cudaErrorInvalidValue;

@@ -7,28 +7,30 @@
 //
 // Weights are E4M3 with a float32 scale per 128 x 128 block, activations bf16.
 // With a few tokens the layer is bound by reading each chosen expert's weights
-// once, so both kernels stream them (fp8_stream.cuh) against up to 32 tokens.
-// Activations enter the E4M3 MMAs without being quantized to E4M3: a value v of
-// a 128-k block, scaled by a power of two that puts the block's largest into
-// [128, 256), is written as v1 + v2 / 16 (+ v3 / 256), each an E4M3 number, the
-// rounded remainder of the one before.  Each term is a column of the MMA's B
-// operand of its own, with its power of two in the column's scale, and the
-// columns of a token are added at the end.  Four bits a term: two terms hold a
-// bf16 activation exactly where it is at least 2^-13 of the block's largest,
-// and to 2^-21 of that largest below; three hold h to 2^-12 of itself.
-// (f16 MMAs need 8 conversions per 16 weights and half the MMA rate, and are no
-// faster: 322 us against 307 on the 128-expert layer, T = 64.)
-//   gate-up  item = (group of tokens of one expert, 8 CG columns of h): MMA
-//            rows 0-7 are gate rows, rows 8-15 the up rows of the same columns,
-//            so a thread ends with both and forms silu(gate) * up.  With few
-//            items, KS = 8 / CG warps share a column tile's K and join their
-//            sums in shared memory.
-//   down     a cluster of CTAs owns 128 rows of W_down (16 per warp) for all
-//            tokens; each CTA takes a share of the (group, k block) units and
-//            sums p * result per token in shared memory; the CTAs' sums are
-//            joined in rank order over distributed shared memory.
+// once, so both kernels stream them through tcgen05 (fp8_skinny.cuh) against up
+// to 32 tokens.  Activations enter the E4M3 MMAs without being quantized to E4M3:
+// a value v of a 128-k block, scaled by a power of two that puts the block's
+// largest into [128, 256), is written as v1 + v2 / 16 (+ v3 / 256), each an E4M3
+// number, the rounded remainder of the one before.  Each term is a column of the
+// MMA's B operand of its own, and the columns of a token are added at the end
+// with its power of two.  Four bits a term: two terms hold a bf16 activation
+// exactly where it is at least 2^-13 of the block's largest, and to 2^-21 of that
+// largest below; three hold h to 2^-12 of itself.
+//   gate-up  item = (group of tokens of one expert, 64 columns of h): the unit's
+//            128 rows are 16 gate rows, the 16 up rows of the same columns, and so
+//            on, so gate and up of a column meet in one warp.  Each CTA walks a
+//            share of the items; with few of them a cluster shares an item's K
+//            and joins its sums over distributed shared memory.
+//   down     a cluster of CTAs owns 128 rows of W_down for all tokens; each CTA
+//            takes a share of the (group, k block) units and sums p * result per
+//            token in shared memory; the CTAs' sums are joined in rank order over
+//            distributed shared memory.
+// Warps of a CTA: 0-3 sums, 4 copies (one thread), 5 MMAs (one thread) and TMEM,
+// 6-9 form the columns, a unit each in turn.  Both kernels derive the routing from
+// the logits by themselves: down does it, and fills its ring with weights, before
+// gate-up has ended.
 // No atomics touch results; the order of every sum follows from the routing.
-#include "fp8_stream.cuh"
+#include "fp8_skinny.cuh"
 
 namespace sharq {
 namespace fp8 {
@@ -37,40 +39,44 @@ constexpr int kMoeMaxTokens = 64, kMoeMaxTopk = 16, kMoeMaxExperts = 512;
 
 namespace {
 
-constexpr int kMoeWarps = 8;
+constexpr int kFormWarps = 4, kFirstFormWarp = kSumWarps + 2;
+constexpr int kMoeWarps = kFirstFormWarp + kFormWarps;
 constexpr int kMoeThreads = 32 * kMoeWarps;
 constexpr int kMaxPairs = kMoeMaxTokens * kMoeMaxTopk;
 
 struct MoeArgs {
   const __nv_bfloat16* x;   // [T][H]
   const float* logits;      // [T][E]
-  const uint8_t* w13;       // [E][2 I][H]: gate rows, then up rows
-  const float* s13;         // [E][blocks(2 I)][blocks(H)]
-  const uint8_t* w2;        // [E][H][I]
+  const float* s13;         // [E][blocks(2 I)][blocks(H)]: gate rows, then up rows
   const float* s2;          // [E][blocks(H)][blocks(I)]
   __nv_bfloat16* y;         // [T][H]
   int* ids;                 // [T][topk] or nullptr
   float* weights;           // [T][topk] or nullptr
-  int* route;               // workspace: the routing that the down kernel reads
+  int* err;                 // workspace: the error word
   float* h;                 // workspace: [T * topk][I]
   long long ldx, ldl, ldy;
   int T, E, topk, H, I, renorm;
+  int splits;               // CTAs of a cluster
 };
 
 // The routing in shared memory: per expert the (token, choice) pairs
-// t * topk + j that chose it, cut into groups of at most 32.
-constexpr int kGroup = 32;
+// t * topk + j that chose it, cut into groups of at most G tokens.  G = 8 for
+// calls of up to 8 tokens, whose groups never hold more.
+constexpr int kSmallGroup = 8, kGroup = 32;
 constexpr int kMaxGroups = kMoeMaxExperts + kMaxPairs / kGroup;
 struct Routing {
   int n_groups;
   short expert[kMaxGroups];  // ascending
   short first[kMaxGroups];   // first of the group's pairs
   short count[kMaxGroups];
-  short pairs[kMaxPairs];    // pair ids, expert by expert
+  short pairs[kMaxPairs];    // pair ids, expert by expert, by token
   float p[kMaxPairs];        // by pair id
 };
-static_assert(sizeof(Routing) % 4 == 0, "copied as ints");
-constexpr int kRouteInts = (int)(sizeof(Routing) / 4);
+struct RoutingScratch {
+  unsigned long long chose[kMoeMaxExperts];  // bit t: token t chose the expert
+  short first[kMoeMaxExperts];
+  short expert_of[kMaxPairs];
+};
 
 // Order-preserving key of a logit: larger logit, larger key; -0 equals +0; a
 // NaN sorts below everything, so an index is always valid.
@@ -89,10 +95,10 @@ __device__ __forceinline__ float logit_exp(float l, float mx) {
   return l == mx ? 1.0f : expf(l - mx);
 }
 
-// Every CTA derives the same routing from the logits.  expert_of: scratch
-// [kMaxPairs]; cnt: scratch [kMoeMaxExperts].  kPer: logits per lane.
+// The k largest logits of a token and their weights, a warp per token.  kPer:
+// logits per lane.
 template <int kPer>
-__device__ void choose_experts(const MoeArgs& a, Routing& r, short* expert_of, int* cnt) {
+__device__ void choose_experts(const MoeArgs& a, Routing& r, RoutingScratch& sc, bool publish) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   for (int t = warp; t < a.T; t += kMoeWarps) {
     const float* lg = a.logits + (size_t)t * a.ldl;
@@ -101,7 +107,7 @@ __device__ void choose_experts(const MoeArgs& a, Routing& r, short* expert_of, i
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       const int e = lane + 32 * i;
-      l[i] = e < a.E ? lg[e] : -INFINITY;
+      l[i] = e < a.E ? __ldcg(lg + e) : -INFINITY;
       key[i] = e < a.E ? max(logit_key(l[i]), 1u) : 0u;  // 0: absent, or taken
       if (l[i] > lmax) lmax = l[i];
     }
@@ -145,9 +151,9 @@ __device__ void choose_experts(const MoeArgs& a, Routing& r, short* expert_of, i
       const int pr = t * a.topk + lane;
       const float p = sum > 0.0f ? __fdiv_rn(mine, sum) : 0.0f;  // no logit above -inf: no expert counts
       r.p[pr] = p;
-      expert_of[pr] = (short)my_e;
-      atomicAdd(&cnt[my_e], 1);
-      if (blockIdx.x == 0) {
+      sc.expert_of[pr] = p > 0.0f ? (short)my_e : (short)-1;  // weight 0: the expert is not evaluated
+      if (p > 0.0f) atomicOr(&sc.chose[my_e], 1ull << t);
+      if (publish) {
         if (a.ids) a.ids[pr] = my_e;
         if (a.weights) a.weights[pr] = p;
       }
@@ -155,467 +161,498 @@ __device__ void choose_experts(const MoeArgs& a, Routing& r, short* expert_of, i
   }
 }
 
-__device__ void build_routing(const MoeArgs& a, Routing& r, short* expert_of, int* cnt) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  for (int e = threadIdx.x; e < a.E; e += kMoeThreads) cnt[e] = 0;
+// Every CTA derives the same routing.  Ends with a barrier.
+template <int G>
+__device__ void build_routing(const MoeArgs& a, Routing& r, RoutingScratch& sc, bool publish) {
+  for (int e = threadIdx.x; e < a.E; e += kMoeThreads) sc.chose[e] = 0ull;
   __syncthreads();
   if (a.E <= 128)
-    choose_experts<4>(a, r, expert_of, cnt);
+    choose_experts<4>(a, r, sc, publish);
   else
-    choose_experts<kMoeMaxExperts / 32>(a, r, expert_of, cnt);
+    choose_experts<kMoeMaxExperts / 32>(a, r, sc, publish);
   __syncthreads();
-  if (warp == 0) {  // lay the experts' pairs out one after another, in groups
-    int ng = 0, np = 0;
-    for (int e0 = 0; e0 < a.E; e0 += 32) {
-      const int e = e0 + lane;
-      const int c = e < a.E ? cnt[e] : 0;
-      const int g = (c + kGroup - 1) / kGroup;
-      int pc = c, pg = g;
+  if (threadIdx.x < 32) {  // lay the experts' pairs out one after another, in groups; a run of experts per lane
+    const int per = (a.E + 31) / 32, e0 = threadIdx.x * per, e1 = min(a.E, e0 + per);
+    int sum = 0;  // pairs in the low half, groups in the high
+    for (int e = e0; e < e1; ++e) {
+      const int c = __popcll(sc.chose[e]);
+      sum += c + ((c + G - 1) / G << 16);
+    }
+    int at = sum;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int c1 = __shfl_up_sync(0xffffffffu, pc, o), g1 = __shfl_up_sync(0xffffffffu, pg, o);
-        if (lane >= o) {
-          pc += c1;
-          pg += g1;
-        }
-      }
-      for (int i = 0; i < g; ++i) {
-        const int at = ng + pg - g + i;
-        r.expert[at] = (short)e;
-        r.first[at] = (short)(np + pc - c + i * kGroup);
-        r.count[at] = (short)min(kGroup, c - i * kGroup);
-      }
-      if (e < a.E) cnt[e] = np + pc - c;  // now the expert's next free place
-      ng += __shfl_sync(0xffffffffu, pg, 31);
-      np += __shfl_sync(0xffffffffu, pc, 31);
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, at, o);
+      if ((int)threadIdx.x >= o) at += v;
     }
-    if (lane == 0) r.n_groups = ng;
+    if (threadIdx.x == 31) r.n_groups = at >> 16;
+    at -= sum;
+    int np = at & 0xffff, ng = at >> 16;
+    for (int e = e0; e < e1; ++e) {
+      const int c = __popcll(sc.chose[e]);
+      sc.first[e] = (short)np;
+      for (int i = 0; i < c; i += G) {
+        r.expert[ng] = (short)e;
+        r.first[ng] = (short)(np + i);
+        r.count[ng++] = (short)min(G, c - i);
+      }
+      np += c;
+    }
   }
   __syncthreads();
-  // A pair's place among its expert's is its rank by pair id: every CTA cuts
-  // the groups alike.  One warp, 32 pairs a step.
-  if (warp == 0) {
-    for (int i0 = 0; i0 < a.T * a.topk; i0 += 32) {
-      const int i = i0 + lane;
-      const int e = i < a.T * a.topk ? expert_of[i] : -1;
-      const uint32_t same = __match_any_sync(0xffffffffu, e);
-      const int before = __popc(same & ((1u << lane) - 1u));
-      const int base = e >= 0 ? cnt[e] : 0;
-      __syncwarp();
-      if (e >= 0) {
-        r.pairs[base + before] = (short)i;
-        if (before == 0) cnt[e] = base + __popc(same);
-      }
-      __syncwarp();
-    }
+  for (int i = threadIdx.x; i < a.T * a.topk; i += kMoeThreads) {
+    const int e = sc.expert_of[i], t = i / a.topk;
+    if (e >= 0) r.pairs[sc.first[e] + __popcll(sc.chose[e] & ((1ull << t) - 1))] = (short)i;
   }
   __syncthreads();
 }
 
-// ----------------------------------------------------- staged activations ---
-// Columns of the MMA's B operand.  A token's terms lie so that one lane's
-// accumulators hold them all: two terms in neighbouring columns, three in the
-// same column of three tiles.  Rows are padded by 16 bytes so that the 8 x 4
-// lanes of an operand read distinct banks.
+// ------------------------------------------------------ columns on the fly ---
+// A form for P tokens (8, 16 or 32) has J P columns, term j of token t at j P + t.
 
-template <int J>
-__device__ __forceinline__ int term_column(int n, int j) {
-  return J == 2 ? 2 * n + j : 8 * (J * (n >> 3) + j) + (n & 7);
-}
-
-__host__ __device__ constexpr int stage_window(int bytes, int nt) {  // 128-k blocks that fit
-  const int w = (bytes / (8 * nt) - 16) / kBlock;
-  return w > 32 ? 32 : w;
-}
-constexpr int kStageScales = 272;  // columns x window of the largest form, rounded up
-
-struct Stage {
-  uint8_t* v;    // [column][row_bytes]
-  float* scale;  // [block][columns]
-  int cols, row_bytes;
+// eight values as they lie in memory
+template <class T>
+struct Raw8 {
+  uint4 v[sizeof(T) / 2];
+  __device__ __forceinline__ void load(const T* p) {
+#pragma unroll
+    for (int i = 0; i < (int)(sizeof(T) / 2); ++i) v[i] = __ldcg(reinterpret_cast<const uint4*>(p) + i);
+  }
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int i = 0; i < (int)(sizeof(T) / 2); ++i) v[i] = make_uint4(0u, 0u, 0u, 0u);
+  }
+  __device__ __forceinline__ void floats(float (&f)[8]) const {
+    if constexpr (sizeof(T) == 2) {
+      unpack_bf16x8(v[0], f);
+    } else {
+      const uint32_t w[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(w[i]);
+    }
+  }
 };
 
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&f)[8]) {
-  unpack_bf16x8(*reinterpret_cast<const uint4*>(p), f);
-}
-__device__ __forceinline__ void load8(const float* p, float (&f)[8]) {
-  const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
-  f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
-}
-
-// Columns of np tokens, blocks [b0, b0 + nb).  rows(n): token n's row.  Half a
-// warp per (token, block), eight values a lane.  Columns of no token keep what
-// they held: their sums are not used.
+// Block b of np tokens into a stage's B operand (128-byte swizzle) and scales, by
+// one warp: half a warp per token, eight values a lane.  rows(n): token n's row.
+// Columns of no token keep what they held: their sums are not used.
 template <int J, class T, class Rows>
-__device__ __forceinline__ void stage_tokens(const Stage& st, int np, int b0, int nb, int K, Rows rows) {
-  const int l16 = threadIdx.x & 15;
-  const int n_items = np * nb;
-  for (int i0 = (threadIdx.x >> 5) * 2; i0 < n_items; i0 += 2 * kMoeWarps) {  // uniform over the warp
-    const int i = i0 + ((threadIdx.x >> 4) & 1);
-    const int n = i / nb, b = i - n * nb;
-    const int k = (b0 + b) * kBlock + l16 * 8;
-    float f[8] = {};
-    if (i < n_items && k < K) load8(static_cast<const T*>(rows(n)) + k, f);
-    float m = 0.0f;
+__device__ __forceinline__ void form_columns(uint8_t* dst, float* scale, int np, int P, int b, int K, Rows rows) {
+  const int lane = threadIdx.x & 31, l16 = lane & 15, half = lane >> 4;
+  const int k = b * kBlock + l16 * 8;
+  constexpr int kBatch = 4;  // loads in flight per lane
+  for (int n0 = 0; n0 < np; n0 += 2 * kBatch) {
+    Raw8<T> raw[kBatch];  // every load is on its way before the first value is used
 #pragma unroll
-    for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(f[j]));
+    for (int i = 0; i < kBatch; ++i) {
+      const int n = n0 + 2 * i + half;
+      raw[i].clear();
+      if (n < np && k < K) raw[i].load(static_cast<const T*>(rows(n)) + k);
+    }
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    // 2^(7 - floor(log2 m)) from the exponent field; the clamp keeps it and its
-    // inverse normal numbers (16^-2 of the inverse included)
-    const uint32_t ef = max(__float_as_uint(m) >> 23, 20u);
-    const float up = __uint_as_float((261u - ef) << 23);
-    // an infinity saturates in E4M3: it is in the scale
-    float s = ef == 255u ? INFINITY : __uint_as_float((ef - 7u) << 23);
+    for (int i = 0; i < kBatch; ++i) {
+      const int n = n0 + 2 * i + half;
+      if (n0 + 2 * i >= np) break;  // uniform over the warp
+      float f[8];
+      raw[i].floats(f);
+      float m = 0.0f;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) f[e] *= up;
+      for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(f[e]));
 #pragma unroll
-    for (int j = 0; j < J; ++j) {
-      const uint32_t c0 = e4m3x4(f[0], f[1], f[2], f[3]), c1 = e4m3x4(f[4], f[5], f[6], f[7]);
-      if (i < n_items) {
-        const int col = term_column<J>(n, j);
-        *reinterpret_cast<uint2*>(st.v + (size_t)col * st.row_bytes + b * kBlock + l16 * 8) = make_uint2(c0, c1);
-        if (l16 == 0) st.scale[b * st.cols + col] = s;
-      }
-      if (j + 1 < J) {
-        const float2 d0 = e4m3x2_to_float(c0), d1 = e4m3x2_to_float(c0 >> 16);
-        const float2 d2 = e4m3x2_to_float(c1), d3 = e4m3x2_to_float(c1 >> 16);
-        f[0] = (f[0] - d0.x) * 16.0f, f[1] = (f[1] - d0.y) * 16.0f;
-        f[2] = (f[2] - d1.x) * 16.0f, f[3] = (f[3] - d1.y) * 16.0f;
-        f[4] = (f[4] - d2.x) * 16.0f, f[5] = (f[5] - d2.y) * 16.0f;
-        f[6] = (f[6] - d3.x) * 16.0f, f[7] = (f[7] - d3.y) * 16.0f;
-        s *= 0.0625f;
+      for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+      // 2^(7 - floor(log2 m)) from the exponent field; the clamp keeps it and its inverse normal numbers
+      const uint32_t ef = max(__float_as_uint(m) >> 23, 20u);
+      const float up = __uint_as_float((261u - ef) << 23);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[e] *= up;
+      if (n < np && l16 == 0)  // an infinity saturates in E4M3: it is in the scale
+        scale[n] = ef == 255u ? INFINITY : __uint_as_float((ef - 7u) << 23);
+#pragma unroll
+      for (int j = 0; j < J; ++j) {
+        const uint32_t c0 = e4m3x4(f[0], f[1], f[2], f[3]), c1 = e4m3x4(f[4], f[5], f[6], f[7]);
+        if (n < np) {
+          const uint32_t row = (uint32_t)(j * P + n);
+          *reinterpret_cast<uint2*>(dst + codes_chunk_off(row, l16 >> 1) + (l16 & 1) * 8) = make_uint2(c0, c1);
+        }
+        if (j + 1 < J) {
+          const float2 d0 = e4m3x2_to_float(c0), d1 = e4m3x2_to_float(c0 >> 16);
+          const float2 d2 = e4m3x2_to_float(c1), d3 = e4m3x2_to_float(c1 >> 16);
+          f[0] = (f[0] - d0.x) * 16.0f, f[1] = (f[1] - d0.y) * 16.0f;
+          f[2] = (f[2] - d1.x) * 16.0f, f[3] = (f[3] - d1.y) * 16.0f;
+          f[4] = (f[4] - d2.x) * 16.0f, f[5] = (f[5] - d2.y) * 16.0f;
+          f[6] = (f[6] - d3.x) * 16.0f, f[7] = (f[7] - d3.y) * 16.0f;
+        }
       }
     }
   }
 }
 
-// ------------------------------------------------------------- ring units ---
+__host__ __device__ constexpr int mma_n(int cols) { return (cols + 15) / 16 * 16; }
+__device__ __forceinline__ int tokens_form(int np) { return np <= 8 ? 8 : (np <= 16 ? 16 : 32); }
 
-constexpr int kUnitBytes = kWeightUnit + 16;  // 16 rows x 128 bytes, and the unit's scales
-
-__device__ __forceinline__ void unit_load(uint32_t slot, const uint8_t* p0, const uint8_t* p1, int left,
-                                          const float* s0, const float* s1, int lane) {
-  rows16_load(slot, p0, p1, left, lane);
-  if (lane < 2) copy4(slot + kWeightUnit + lane * 4, lane ? s1 : s0);
+// One finished unit's sums: acc[t] += (c1 + c2 / 16 (+ c3 / 256)) scale[t] s_w
+template <int J, int P, int kStages>
+__device__ __forceinline__ bool add_unit(SkinnyBars<kStages>& bars, RingPos<kStages>& pos, uint32_t tmem_lane,
+                                         int stage_cols, const float* scale, float s_w, float (&acc)[P],
+                                         uint64_t deadline, int lane) {
+  if (!wait_done(bars, pos, deadline)) return false;
+  uint32_t v[J * P];
+  tmem_read(tmem_lane + pos.s * stage_cols, v);
+  tmem_ld_wait();
+#pragma unroll
+  for (int t = 0; t < P; t += 4) {
+    const float4 s4 = *reinterpret_cast<const float4*>(scale + t);
+    const float s[4] = {s4.x, s4.y, s4.z, s4.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float c = __uint_as_float(v[(J - 1) * P + t + i]);
+#pragma unroll
+      for (int j = J - 2; j >= 0; --j) c = fmaf(c, 0.0625f, __uint_as_float(v[j * P + t + i]));
+      acc[t + i] = fmaf(c, s[i] * s_w, acc[t + i]);
+    }
+  }
+  release_unit(bars, pos, lane);
+  pos.next();
+  return true;
 }
 
-// acc += unit x staged block b, for NT tiles of eight columns: rows g take
-// weight scale s.x, rows g + 8 scale s.y
-template <int NT>
-__device__ __forceinline__ void unit_product(uint32_t slot, const Stage& st, int b, int lane, float (&acc)[NT][4]) {
-  const int g = lane >> 2, q = lane & 3;
-  WeightUnit w;
-  w.read(slot, lane);
-  const float2 s = lds_f2(slot + kWeightUnit);
-  const uint32_t x = smem_u32(st.v) + g * st.row_bytes + b * kBlock + q * 16;
-  const uint32_t xs = smem_u32(st.scale) + (b * st.cols + 2 * q) * 4;
-#pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    float c[4];
-    const uint32_t p = x + 8 * n * st.row_bytes;
-    w.times(lds128(p), lds128(p + 64), c);
-    const float2 t = lds_f2(xs + 32 * n);
-    acc[n][0] = fmaf(c[0], t.x * s.x, acc[n][0]);
-    acc[n][1] = fmaf(c[1], t.y * s.x, acc[n][1]);
-    acc[n][2] = fmaf(c[2], t.x * s.y, acc[n][2]);
-    acc[n][3] = fmaf(c[3], t.y * s.y, acc[n][3]);
+template <int J, int G, int Stages>
+struct MoeRing {
+  static constexpr int kStages = Stages;
+  static constexpr int kCols = mma_n(J * G);
+  static constexpr int kStageBytes = kUnitBytes + kCols * kBlock;
+  static constexpr int kTmem = tmem_cols(kCols * kStages);
+  static constexpr int kBytes = kStages * kStageBytes;
+  static_assert(kTmem <= 512 && kStageBytes % 1024 == 0, "ring");
+};
+
+template <int P>
+struct Tokens {
+  static constexpr int value = P;
+};
+
+// start-up common to both kernels: barriers, TMEM
+template <class R>
+__device__ __forceinline__ void moe_setup(SkinnyBars<R::kStages>& bars, const CUtensorMap* map) {
+  if (threadIdx.x == kSumWarps * 32) {
+    tma_prefetch_map(map);
+    bars.init(2);
+  }
+  if (threadIdx.x >> 5 == kSumWarps + 1) {
+    tmem_alloc(&bars.tmem, R::kTmem);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+}
+template <class R>
+__device__ __forceinline__ void moe_teardown(uint32_t tmem) {
+  tc_fence_before();
+  __syncthreads();
+  if (threadIdx.x >> 5 == kSumWarps + 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, R::kTmem);
   }
 }
 
 // ---------------------------------------------------------------- gate-up ---
 
-constexpr int kUpTerms = 2;
-constexpr int kUpRing = 4;
-struct UpSmem {  // offsets in dynamic shared memory
-  static constexpr int kStageBytes = 34816;
-  static constexpr int kRing = 0;
-  static constexpr int kStage = kRing + kMoeWarps * kUpRing * kUnitBytes;
-  static constexpr int kScale = kStage + kStageBytes;
-  static constexpr int kBytes = kScale + kStageScales * 4;
-};
-__host__ __device__ constexpr int join_row(int nt) { return 4 * nt + 1; }
-static_assert(kMoeWarps * 16 * join_row(kGroup * kUpTerms / 8) * 4 <= UpSmem::kStageBytes, "join buffer");
-static_assert(8 * 8 * stage_window(UpSmem::kStageBytes, 8) <= kStageScales &&
-              8 * stage_window(UpSmem::kStageBytes, 1) <= kStageScales, "column scales");
-
-struct UpWalk {  // one warp's sequence of units
-  const MoeArgs& a;
-  const Routing& r;
-  int it, end, kb, ks, KS, CG, cg, tiles, nkb, rb;
-  const uint8_t *wg, *wu;
-  const float *sg, *su;
-  bool on;
-  __device__ __forceinline__ void item(int lane) {
-    if (it >= end) return;
-    const int grp = it / tiles, i0 = ((it - grp * tiles) * CG + cg) * 8;
-    on = i0 < a.I;
-    if (!on) return;
-    const int e = r.expert[grp];
-    wg = a.w13 + ((size_t)e * 2 * a.I + i0 + (lane >> 2)) * a.H + 16 * (lane & 3);
-    wu = wg + (size_t)a.I * a.H;
-    sg = a.s13 + ((size_t)e * rb + i0 / kBlock) * nkb;
-    su = a.s13 + ((size_t)e * rb + (a.I + i0) / kBlock) * nkb;
-  }
-  __device__ __forceinline__ void issue(uint32_t slot, int lane) {
-    if (it < end) {
-      const int k = kb * kBlock;
-      if (on) unit_load(slot, wg + k, wu + k, a.H - k - 16 * (lane & 3), sg + kb, su + kb, lane);
-      kb += KS;
-      if (kb >= nkb) {
-        kb = ks;
-        ++it;
-        item(lane);
-      }
-    }
-    copies_commit();
-  }
+constexpr int kUpTerms = 2, kUpCols = 64;
+template <int G>
+struct Up : MoeRing<kUpTerms, G, G == kSmallGroup ? 5 : 8> {
+  // several CTAs of the small form, and down's beside them, reside on an SM
+  static constexpr int kSmemBytes = Up::kBytes + 1024;
 };
 
-template <int NT>
-__device__ __forceinline__ void up_item(const MoeArgs& a, const Routing& r, UpWalk& walk, int it, uint8_t* smem,
-                                        uint32_t ring, uint32_t& slot, int& staged) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int g = lane >> 2, q = lane & 3;
-  const int grp = it / walk.tiles, base = (it - grp * walk.tiles) * walk.CG * 8;
-  const bool on = base + walk.cg * 8 < a.I;
-  const int p0 = r.first[grp], np = r.count[grp];
-  constexpr int kWin = stage_window(UpSmem::kStageBytes, NT);
-  const Stage st{smem + UpSmem::kStage, reinterpret_cast<float*>(smem + UpSmem::kScale), 8 * NT, kWin * kBlock + 16};
-  float acc[NT][4] = {};
-  int kb = walk.ks;
-  for (int b0 = 0; b0 < walk.nkb; b0 += kWin) {
-    const int nb = min(kWin, walk.nkb - b0);
-    if (staged != grp) {  // otherwise the previous item left the same tokens here
-      __syncthreads();
-      stage_tokens<kUpTerms, __nv_bfloat16>(st, np, b0, nb, a.H, [&](int n) {
-        return a.x + (size_t)(r.pairs[p0 + n] / a.topk) * a.ldx;
-      });
-      __syncthreads();
-    }
-    for (; kb < b0 + nb; kb += walk.KS) {
-      copies_wait<kUpRing - 1>();
-      __syncwarp();  // the scales come from other lanes' copies
-      if (on) unit_product<NT>(slot, st, kb - b0, lane, acc);
-      __syncwarp();
-      walk.issue(slot, lane);
-      slot = slot == ring + (kUpRing - 1) * kUnitBytes ? ring : slot + kUnitBytes;
-    }
-  }
-  staged = walk.nkb <= kWin ? grp : -1;
-  // columns 2 q, 2 q + 1 of tile n are the two terms of token 4 n + q
-  if (walk.KS == 1) {
-    if (on) {
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        const int m = 4 * n + q;
-        if (m < np)
-          a.h[(size_t)r.pairs[p0 + m] * a.I + base + walk.cg * 8 + g] =
-              silu_mul(acc[n][0] + acc[n][1], acc[n][2] + acc[n][3]);
-      }
-    }
-    return;
-  }
-  __syncthreads();  // the stage has been read: the warps' sums take its place
-  staged = -1;
-  float* red = reinterpret_cast<float*>(smem + UpSmem::kStage);
-  constexpr int kRow = join_row(NT);
-#pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    red[(warp * 16 + g) * kRow + 4 * n + q] = acc[n][0] + acc[n][1];
-    red[(warp * 16 + g + 8) * kRow + 4 * n + q] = acc[n][2] + acc[n][3];
-  }
-  __syncthreads();
-  for (int i = threadIdx.x; i < walk.CG * 8 * np; i += kMoeThreads) {
-    const int m = i / (walk.CG * 8), col = i - m * walk.CG * 8;
-    if (base + col >= a.I) continue;
-    float gs = 0.0f, us = 0.0f;
-    for (int k = 0; k < walk.KS; ++k) {
-      const float* row = red + (((col >> 3) * walk.KS + k) * 16 + (col & 7)) * kRow + m;
-      gs += row[0];
-      us += row[8 * kRow];
-    }
-    a.h[(size_t)r.pairs[p0 + m] * a.I + base + col] = silu_mul(gs, us);
-  }
-}
-
-__global__ void __launch_bounds__(kMoeThreads, 2) moe_gate_up_kernel(const MoeArgs a) {
+template <int G>
+__global__ void __launch_bounds__(kMoeThreads, G == kSmallGroup ? 2 : 1)
+    moe_gate_up_kernel(const __grid_constant__ CUtensorMap map, const MoeArgs a) {
+  using C = Up<G>;
+  using Pos = RingPos<C::kStages>;
+  extern __shared__ uint8_t smem_raw[];
   __shared__ Routing r;
-  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ __align__(8) SkinnyBars<C::kStages> bars;
+  __shared__ __align__(16) float scale[C::kStages][G];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  moe_setup<C>(bars, &map);
+  const uint32_t tmem = bars.tmem;
   pdl_wait();
-  {  // scratch of the routing: the ring, not in use yet
-    int* cnt = reinterpret_cast<int*>(smem);
-    build_routing(a, r, reinterpret_cast<short*>(cnt + kMoeMaxExperts), cnt);
+  build_routing<G>(a, r, *reinterpret_cast<RoutingScratch*>(smem), blockIdx.x == 0);
+  pdl_trigger();  // after the allocation, and after the logits of the kernels before are complete
+  const int nkb = blocks_of(a.H), tiles = (a.I + kUpCols - 1) / kUpCols, items = r.n_groups * tiles;
+  const int S = a.splits, rank = S > 1 ? (int)cluster_ctarank() : 0;
+  const int cl = (int)blockIdx.x / S, ncl = (int)gridDim.x / S;  // with S > 1 there are as many clusters as items
+  const int it0 = (int)((long long)cl * items / ncl), it1 = (int)((long long)(cl + 1) * items / ncl);
+  const int b0 = rank * nkb / S, b1 = (rank + 1) * nkb / S;
+  const uint64_t deadline = globaltimer_ns() + kWaitNs;
+  fence_proxy_async_smem();  // the scratch was written where copies land
+  __syncthreads();
+
+  if (warp == kSumWarps) {
+    if (elect_one()) {
+      Pos p;
+      int n = 0;
+      for (int it = it0; it < it1 && !bars.abort; ++it) {
+        const int grp = it / tiles, i0 = (it - grp * tiles) * kUpCols, e = r.expert[grp];
+        for (int b = b0; b < b1; ++b, ++n, p.next()) {
+          if (!wait_empty(bars, p, deadline)) {
+            bars.give_up(a.err);
+            break;
+          }
+          uint8_t* st = smem + p.s * C::kStageBytes;
+          mbar_arrive_expect_tx(&bars.full[p.s], kUnitBytes);
+#pragma unroll
+          for (int w = 0; w < kUpCols / 16; ++w)
+            tma_4d(st + w * 32 * kBlock, &map, b * kBlock, i0 + 16 * w, 0, e, &bars.full[p.s]);
+        }
+      }
+      if (bars.abort) drain_copies(bars, n);
+    }
+  } else if (warp == kSumWarps + 1) {
+    if (elect_one()) {
+      Pos p;
+      for (int it = it0; it < it1 && !bars.abort; ++it) {
+        const uint32_t idesc = idesc_e4m3(kUnitRows, mma_n(kUpTerms * tokens_form(r.count[it / tiles])));
+        for (int b = b0; b < b1; ++b, p.next()) {
+          if (!mbar_wait(&bars.full[p.s], p.phase, deadline, &bars.abort)) {
+            bars.give_up(a.err);
+            break;
+          }
+          tc_fence_after();
+          unit_mma(tmem + p.s * C::kCols, smem_u32(smem + p.s * C::kStageBytes), idesc);
+          tc_commit(&bars.done[p.s]);
+        }
+      }
+    }
+  } else if (warp >= kFirstFormWarp) {
+    Pos p;
+    int turn = warp - kFirstFormWarp;  // units until this warp's next
+    for (int it = it0; it < it1 && !bars.abort; ++it) {
+      const int grp = it / tiles, np = r.count[grp], p0 = r.first[grp], P = tokens_form(np);
+      for (int b = b0; b < b1; ++b, p.next()) {
+        if (turn-- > 0) continue;
+        turn = kFormWarps - 1;
+        if (!__all_sync(0xffffffffu, wait_empty(bars, p, deadline))) {
+          bars.give_up(a.err);
+          break;
+        }
+        form_columns<kUpTerms, __nv_bfloat16>(smem + p.s * C::kStageBytes + kUnitBytes, scale[p.s], np, P, b, a.H,
+                                              [&](int n) { return a.x + (size_t)(r.pairs[p0 + n] / a.topk) * a.ldx; });
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cta(&bars.full[p.s]);
+      }
+    }
+  } else {
+    Pos p;
+    const int rb = blocks_of(2 * a.I);
+    const uint32_t tmem_lane = tmem + ((uint32_t)(warp * 32) << 16);
+    for (int it = it0; it < it1 && !bars.abort; ++it) {
+      const int grp = it / tiles, c0 = (it - grp * tiles) * kUpCols + 16 * warp;
+      const int np = r.count[grp], p0 = r.first[grp];
+      // the warp's 16 gate rows lie in one scale block, its up rows in another; rows past the last read zeros
+      const float* s13 = a.s13 + (size_t)r.expert[grp] * rb * nkb;
+      const int row = min(c0, a.I - 16);
+      ScaleRow sg, su;
+      sg.start(s13 + (size_t)(row / kBlock) * nkb, nkb, b0, lane);
+      su.start(s13 + (size_t)((a.I + row) / kBlock) * nkb, nkb, b0, lane);
+      auto run = [&](auto form) {
+        constexpr int P = decltype(form)::value;
+        float acc[P] = {};
+        for (int b = b0; b < b1; ++b) {
+          const float g = sg.at(b, lane), u = su.at(b, lane);
+          if (!add_unit<kUpTerms, P>(bars, p, tmem_lane, C::kCols, scale[p.s], lane < 16 ? g : u, acc, deadline,
+                                     lane)) {
+            bars.give_up(a.err);
+            return;
+          }
+        }
+        if (S == 1) {
+          const int col = c0 + (lane & 15);
+#pragma unroll
+          for (int t = 0; t < P; t += 2) {  // the lower lanes finish token t, the upper ones t + 1
+            const float other = __shfl_xor_sync(0xffffffffu, lane < 16 ? acc[t + 1] : acc[t], 16);
+            const int n = t + (lane >> 4);
+            if (n < np && col < a.I)
+              a.h[(size_t)r.pairs[p0 + n] * a.I + col] =
+                  lane < 16 ? silu_mul(acc[t], other) : silu_mul(other, acc[t + 1]);
+          }
+        } else {  // one item per cluster: the ring is free once every sum warp is here
+          asm volatile("bar.sync 1, 128;" ::: "memory");
+          float* out = reinterpret_cast<float*>(smem);
+#pragma unroll
+          for (int t = 0; t < P; ++t)
+            if (t < np) out[t * kUnitRows + threadIdx.x] = acc[t];
+        }
+      };
+      if (np <= 8)
+        run(Tokens<8>{});
+      else if (G > 8 && np <= 16)
+        run(Tokens<G < 16 ? 8 : 16>{});
+      else if (G > 16)
+        run(Tokens<G < 32 ? 8 : 32>{});
+    }
   }
-  pdl_trigger();
-  if (blockIdx.x == 0) {
-    const int* src = reinterpret_cast<const int*>(&r);
-    for (int i = threadIdx.x; i < kRouteInts; i += kMoeThreads) a.route[i] = src[i];
+  if (S > 1) {
+    cluster_sync_all();  // every CTA's sums are in its shared memory
+    if (it0 < it1 && !bars.abort) {
+      const int grp = it0 / tiles, i0 = (it0 - grp * tiles) * kUpCols, np = r.count[grp], p0 = r.first[grp];
+      const uint32_t base = smem_u32(smem);
+      const int total = np * kUpCols;
+      for (int i = rank * total / S + (int)threadIdx.x; i < (rank + 1) * total / S; i += kMoeThreads) {
+        const int n = i / kUpCols, c = i - n * kUpCols;
+        const uint32_t at = base + (n * kUnitRows + (c >> 4) * 32 + (c & 15)) * 4;
+        float g = 0.0f, u = 0.0f;
+        for (int q = 0; q < S; ++q) {
+          const uint32_t peer = mapa_shared(at, (uint32_t)q);
+          g += ld_shared_cluster_f(peer);
+          u += ld_shared_cluster_f(peer + 64);
+        }
+        if (i0 + c < a.I) a.h[(size_t)r.pairs[p0 + n] * a.I + i0 + c] = silu_mul(g, u);
+      }
+    }
+    cluster_sync_all();  // no CTA leaves while a peer reads its sums
   }
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int nkb = blocks_of(a.H), cols = a.I / 8;
-  // The most warps per column tile that still leave every CTA at most one
-  // item: with few experts all their weights are then in flight at once; with
-  // many items each warp keeps a tile to itself.
-  int KS = 1;
-  while (KS < kMoeWarps && 2 * KS <= nkb &&
-         r.n_groups * ((cols + kMoeWarps / (2 * KS) - 1) / (kMoeWarps / (2 * KS))) <= (int)gridDim.x)
-    KS *= 2;
-  const int CG = kMoeWarps / KS, tiles = (cols + CG - 1) / CG;
-  const int items = r.n_groups * tiles;
-  const int it0 = (int)((long long)blockIdx.x * items / gridDim.x);
-  const int it1 = (int)((long long)(blockIdx.x + 1) * items / gridDim.x);
-  UpWalk walk{a, r, it0, it1, warp % KS, warp % KS, KS, CG, warp / KS, tiles, nkb, blocks_of(2 * a.I),
-              nullptr, nullptr, nullptr, nullptr, false};
-  walk.item(lane);
-  const uint32_t ring = smem_u32(smem + UpSmem::kRing) + warp * kUpRing * kUnitBytes;
-  for (int i = 0; i < kUpRing; ++i) walk.issue(ring + i * kUnitBytes, lane);
-  uint32_t slot = ring;
-  int staged = -1;
-  for (int it = it0; it < it1; ++it) {
-    const int c = r.count[it / tiles] * kUpTerms;
-    if (c <= 8)
-      up_item<1>(a, r, walk, it, smem, ring, slot, staged);
-    else if (c <= 16)
-      up_item<2>(a, r, walk, it, smem, ring, slot, staged);
-    else if (c <= 32)
-      up_item<4>(a, r, walk, it, smem, ring, slot, staged);
-    else
-      up_item<8>(a, r, walk, it, smem, ring, slot, staged);
-  }
-  copies_wait<0>();
+  moe_teardown<C>(tmem);
 }
 
 // ------------------------------------------------------------------- down ---
 
 constexpr int kDownTerms = 3;
-constexpr int kDownRing = 3;
-constexpr int kDownRows = 16 * kMoeWarps;
-struct DownSmem {
-  static constexpr int kStageBytes = 18944;
-  static constexpr int kRing = 0;
-  static constexpr int kStage = kRing + kMoeWarps * kDownRing * kUnitBytes;
-  static constexpr int kScale = kStage + kStageBytes;
-  static constexpr int kSums = kScale + kStageScales * 4;  // [T][128]
-  static constexpr int bytes(int T) { return kSums + T * kDownRows * 4; }
+template <int G>
+struct Down : MoeRing<kDownTerms, G, G == kSmallGroup ? 4 : 5> {
+  static constexpr int kSums = Down::kBytes;  // [T][128]
+  static constexpr int bytes(int T) { return kSums + T * kUnitRows * 4 + 1024; }
 };
-static_assert(stage_window(DownSmem::kStageBytes, kGroup * kDownTerms / 8) >= 1, "a block of a full group must fit");
+static_assert(Up<kSmallGroup>::kSmemBytes + Down<kSmallGroup>::bytes(kSmallGroup) + 2 * (int)sizeof(Routing) <= 226 * 1024 &&
+              Up<kSmallGroup>::kTmem + Down<kSmallGroup>::kTmem <= 512, "both kernels' small forms share an SM");
 
-template <int N>
-struct Int {
-  static constexpr int value = N;
-};
-__device__ __forceinline__ float2 ld_shared_cluster_f2(uint32_t addr) {
-  float2 v;
-  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
-  return v;
-}
-
-__global__ void __launch_bounds__(kMoeThreads, 2) moe_down_kernel(const MoeArgs a, int C) {
+template <int G>
+__global__ void __launch_bounds__(kMoeThreads, G == kSmallGroup ? 2 : 1)
+    moe_down_kernel(const __grid_constant__ CUtensorMap map, const MoeArgs a) {
+  using C = Down<G>;
+  using Pos = RingPos<C::kStages>;
+  extern __shared__ uint8_t smem_raw[];
   __shared__ Routing r;
-  extern __shared__ __align__(16) uint8_t smem[];
-  pdl_trigger();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int g = lane >> 2, q = lane & 3;
-  const int rank = C > 1 ? (int)cluster_ctarank() : 0;
-  const int d0 = (int)(blockIdx.x / C) * kDownRows;
+  __shared__ __align__(8) SkinnyBars<C::kStages> bars;
+  __shared__ __align__(16) float scale[C::kStages][G];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int S = a.splits, rank = S > 1 ? (int)cluster_ctarank() : 0;
+  const int d0 = (int)(blockIdx.x / S) * kUnitRows;
   const int nkb = blocks_of(a.I), rb = blocks_of(a.H);
-  float* sums = reinterpret_cast<float*>(smem + DownSmem::kSums);
-  for (int i = threadIdx.x; i < a.T * kDownRows; i += kMoeThreads) sums[i] = 0.0f;
-  pdl_wait();
-  {
-    int* dst = reinterpret_cast<int*>(&r);
-    for (int i = threadIdx.x; i < kRouteInts; i += kMoeThreads) dst[i] = a.route[i];
-  }
-  __syncthreads();
+  float* sums = reinterpret_cast<float*>(smem + C::kSums);
+  moe_setup<C>(bars, &map);
+  const uint32_t tmem = bars.tmem;
+  pdl_trigger();  // after the allocation
+  // Logits and weights: complete before gate-up let this grid start.
+  build_routing<G>(a, r, *reinterpret_cast<RoutingScratch*>(smem), false);
+  for (int i = threadIdx.x; i < a.T * kUnitRows; i += kMoeThreads) sums[i] = 0.0f;
   const int units = r.n_groups * nkb;
-  const int u0 = (int)((long long)rank * units / C), u1 = (int)((long long)(rank + 1) * units / C);
-  const int row = d0 + warp * 16;
-  const bool on = row < a.H;  // H is a multiple of 16
-  const uint32_t ring = smem_u32(smem + DownSmem::kRing) + warp * kDownRing * kUnitBytes;
-  int lu = u0, lg = u0 / nkb, lb = u0 - lg * nkb;  // the next unit to load: group, block
-  auto issue = [&](uint32_t slot) {
-    if (lu < u1) {
-      if (on) {
-        const int e = r.expert[lg], k = lb * kBlock;
-        const uint8_t* w = a.w2 + ((size_t)e * a.H + row + g) * a.I + k + 16 * q;
-        const float* s = a.s2 + ((size_t)e * rb + row / kBlock) * nkb + lb;
-        unit_load(slot, w, w + (size_t)8 * a.I, a.I - k - 16 * q, s, s, lane);
+  const int u0 = (int)((long long)rank * units / S), u1 = (int)((long long)(rank + 1) * units / S);
+  const uint64_t deadline = globaltimer_ns() + 2 * kWaitNs;  // gate-up may still run
+  fence_proxy_async_smem();  // the scratch was written where copies land
+  __syncthreads();
+
+  if (warp == kSumWarps) {
+    if (elect_one()) {
+      Pos p;
+      int grp = u0 / nkb, b = u0 - grp * nkb, u = u0;
+      for (; u < u1; ++u, p.next()) {
+        if (!wait_empty(bars, p, deadline)) {
+          bars.give_up(a.err);
+          break;
+        }
+        mbar_arrive_expect_tx(&bars.full[p.s], kUnitBytes);
+        tma_2d(smem + p.s * C::kStageBytes, &map, b * kBlock, r.expert[grp] * a.H + d0, &bars.full[p.s]);
+        if (++b == nkb) {
+          b = 0;
+          ++grp;
+        }
       }
-      ++lu;
-      if (++lb == nkb) {
-        lb = 0;
-        ++lg;
+      if (bars.abort) drain_copies(bars, u - u0);
+    }
+  } else if (warp == kSumWarps + 1) {
+    if (elect_one()) {
+      Pos p;
+      for (int u = u0; u < u1; ++u, p.next()) {
+        const uint32_t idesc = idesc_e4m3(kUnitRows, mma_n(kDownTerms * tokens_form(r.count[u / nkb])));
+        if (!mbar_wait(&bars.full[p.s], p.phase, deadline, &bars.abort)) {
+          bars.give_up(a.err);
+          break;
+        }
+        tc_fence_after();
+        unit_mma(tmem + p.s * C::kCols, smem_u32(smem + p.s * C::kStageBytes), idesc);
+        tc_commit(&bars.done[p.s]);
       }
     }
-    copies_commit();
-  };
-  for (int i = 0; i < kDownRing; ++i) issue(ring + i * kUnitBytes);
-  uint32_t slot = ring;
-  for (int u = u0; u < u1;) {
-    const int grp = u / nkb, b0 = u - grp * nkb;
-    const int np = r.count[grp], p0 = r.first[grp];
-    auto run = [&](auto tag) {
-      constexpr int NT = decltype(tag)::value;
-      constexpr int kWin = stage_window(DownSmem::kStageBytes, NT);
-      static_assert(8 * NT * kWin <= kStageScales, "column scales");
-      const int nb = min(min(kWin, nkb - b0), u1 - u);
-      const Stage st{smem + DownSmem::kStage, reinterpret_cast<float*>(smem + DownSmem::kScale), 8 * NT,
-                     kWin * kBlock + 16};
-      __syncthreads();  // the stage has been read
-      stage_tokens<kDownTerms, float>(st, np, b0, nb, a.I, [&](int n) { return a.h + (size_t)r.pairs[p0 + n] * a.I; });
-      __syncthreads();
-      float acc[NT][4] = {};
-      for (int b = 0; b < nb; ++b) {
-        copies_wait<kDownRing - 1>();
-        __syncwarp();
-        if (on) unit_product<NT>(slot, st, b, lane, acc);
-        __syncwarp();
-        issue(slot);
-        slot = slot == ring + (kDownRing - 1) * kUnitBytes ? ring : slot + kUnitBytes;
+  } else if (warp >= kFirstFormWarp) {
+    pdl_wait();  // gate-up has ended: h is complete
+    Pos p;
+    for (int u = u0; u < u1; ++u, p.next()) {
+      if ((u - u0) % kFormWarps != warp - kFirstFormWarp) continue;
+      const int grp = u / nkb, np = r.count[grp], p0 = r.first[grp];
+      if (!__all_sync(0xffffffffu, wait_empty(bars, p, deadline))) {
+        bars.give_up(a.err);
+        break;
       }
-      // An expert appears once in a token's choices, so the columns are
-      // different tokens: no two lanes add to one place, no two warps share a row.
-      if (on) {
-#pragma unroll
-        for (int n = 0; n < NT; n += kDownTerms)
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const int m = (n / kDownTerms) * 8 + 2 * q + c;
-            if (m < np) {
-              const int pc = r.pairs[p0 + m];
-              float* dst = sums + (size_t)(pc / a.topk) * kDownRows + warp * 16 + g;
-              const float p = r.p[pc];
-              dst[0] = fmaf(p, acc[n][c] + acc[n + 1][c] + acc[n + 2][c], dst[0]);
-              dst[8] = fmaf(p, acc[n][2 + c] + acc[n + 1][2 + c] + acc[n + 2][2 + c], dst[8]);
-            }
+      form_columns<kDownTerms, float>(smem + p.s * C::kStageBytes + kUnitBytes, scale[p.s], np, tokens_form(np),
+                                      u - grp * nkb, a.I, [&](int n) { return a.h + (size_t)r.pairs[p0 + n] * a.I; });
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cta(&bars.full[p.s]);
+    }
+  } else {
+    Pos p;
+    const uint32_t tmem_lane = tmem + ((uint32_t)(warp * 32) << 16);
+    for (int u = u0; u < u1 && !bars.abort;) {
+      const int grp = u / nkb, bb = u - grp * nkb, be = min(nkb, bb + u1 - u);
+      const int np = r.count[grp], p0 = r.first[grp];
+      ScaleRow sw;
+      sw.start(a.s2 + ((size_t)r.expert[grp] * rb + d0 / kBlock) * nkb, nkb, bb, lane);
+      auto run = [&](auto form) {
+        constexpr int P = decltype(form)::value;
+        float acc[P] = {};
+        for (int b = bb; b < be; ++b) {
+          const float s = sw.at(b, lane);
+          if (!add_unit<kDownTerms, P>(bars, p, tmem_lane, C::kCols, scale[p.s], s, acc, deadline, lane)) {
+            bars.give_up(a.err);
+            return;
           }
-        __syncwarp();
-      }
-      u += nb;
-    };
-    if (np <= 8)
-      run(Int<3>{});
-    else if (np <= 16)
-      run(Int<6>{});
-    else
-      run(Int<12>{});
+        }
+        // this thread alone adds to its row's sums; an expert appears once in a token's choices
+#pragma unroll
+        for (int n = 0; n < P; ++n)
+          if (n < np) {
+            const int pc = r.pairs[p0 + n];
+            float* dst = sums + (size_t)(pc / a.topk) * kUnitRows + threadIdx.x;
+            *dst = fmaf(r.p[pc], acc[n], *dst);
+          }
+      };
+      if (np <= 8)
+        run(Tokens<8>{});
+      else if (G > 8 && np <= 16)
+        run(Tokens<G < 16 ? 8 : 16>{});
+      else if (G > 16)
+        run(Tokens<G < 32 ? 8 : 32>{});
+      u += be - bb;
+    }
   }
-  copies_wait<0>();
-  if (C > 1)
+  pdl_wait();  // y may be x: no store before gate-up has ended (a CTA without units comes here at once)
+  if (S > 1)
     cluster_sync_all();  // every CTA's sums are complete
   else
     __syncthreads();
   // this CTA's share of the outputs, two neighbouring rows a thread
-  const int pairs_of = a.T * (kDownRows / 2);
-  const int i1 = (int)((long long)(rank + 1) * pairs_of / C);
+  const int pairs_of = a.T * (kUnitRows / 2);
   const uint32_t base = smem_u32(sums);
-  for (int i = (int)((long long)rank * pairs_of / C) + threadIdx.x; i < i1; i += kMoeThreads) {
-    const int t = i / (kDownRows / 2), d = d0 + 2 * (i - t * (kDownRows / 2));
-    if (d >= a.H) continue;
+  for (int i = rank * pairs_of / S + (int)threadIdx.x; i < (rank + 1) * pairs_of / S; i += kMoeThreads) {
+    const int t = i / (kUnitRows / 2), d = d0 + 2 * (i - t * (kUnitRows / 2));
+    if (d >= a.H || bars.abort) continue;
     float2 v = make_float2(0.0f, 0.0f);
-    for (int c = 0; c < C; ++c) {
-      const float2 o = ld_shared_cluster_f2(C > 1 ? mapa_shared(base + i * 8, (uint32_t)c) : base + i * 8);
+    for (int c = 0; c < S; ++c) {
+      const float2 o = ld_shared_cluster_f2(S > 1 ? mapa_shared(base + i * 8, (uint32_t)c) : base + i * 8);
       v.x += o.x;
       v.y += o.y;
     }
@@ -623,14 +660,48 @@ __global__ void __launch_bounds__(kMoeThreads, 2) moe_down_kernel(const MoeArgs 
     y[0] = __float2bfloat16_rn(v.x);
     y[1] = __float2bfloat16_rn(v.y);
   }
-  if (C > 1) cluster_sync_all();  // no CTA leaves while a peer reads its sums
+  if (S > 1) cluster_sync_all();  // no CTA leaves while a peer reads its sums
+  moe_teardown<C>(tmem);
+}
+
+constexpr size_t kErrBytes = 256;
+
+template <int G>
+cudaError_t launch_form(MoeArgs& a, const uint8_t* w13, const uint8_t* w2, const Device* dev, cudaStream_t stream) {
+  using U = Up<G>;
+  using D = Down<G>;
+  CUtensorMap m13, m2;
+  if (!halves_map(&m13, w13, (uint64_t)a.E, (uint64_t)a.I, (uint64_t)a.H, 16) ||
+      !byte_map(&m2, w2, (uint64_t)a.E * a.H, (uint64_t)a.I, kUnitRows))
+    return cudaErrorInvalidValue;
+  static bool up_done[64] = {}, down_done[64] = {};
+  cudaError_t e = opt_in_smem((const void*)moe_gate_up_kernel<G>, U::kSmemBytes, up_done);
+  if (e == cudaSuccess) e = opt_in_smem((const void*)moe_down_kernel<G>, D::bytes(G == kSmallGroup ? G : kMoeMaxTokens), down_done);
+  if (e != cudaSuccess) return e;
+  // Items if every choice were another expert; with few, clusters share them.
+  // Otherwise as many CTAs as reside at once.
+  const int pairs = a.T * a.topk, tiles = (a.I + kUpCols - 1) / kUpCols;
+  const long long most = (long long)(pairs < a.E + pairs / G ? pairs : a.E + pairs / G) * tiles;
+  const int nkb = blocks_of(a.H);
+  a.splits = 1;
+  while (a.splits < 8 && 2 * a.splits <= nkb && 2 * a.splits * most <= dev->sms) a.splits *= 2;
+  const int resident = dev->sms * (G == kSmallGroup ? 2 : 1);
+  void* up_args[] = {&m13, &a};
+  e = launch_pdl((const void*)moe_gate_up_kernel<G>, dim3((unsigned)((most < resident ? most : resident) * a.splits)),
+                 dim3(kMoeThreads), U::kSmemBytes, a.splits, stream, up_args);
+  if (e != cudaSuccess) return e;
+  // the widest cluster with which every CTA has an SM of its own
+  const int row_tiles = (a.H + kUnitRows - 1) / kUnitRows;
+  a.splits = 8;
+  while (a.splits > 1 && row_tiles * a.splits > dev->sms) a.splits /= 2;
+  void* down_args[] = {&m2, &a};
+  return launch_pdl((const void*)moe_down_kernel<G>, dim3((unsigned)(row_tiles * a.splits)), dim3(kMoeThreads),
+                    D::bytes(a.T), a.splits, stream, down_args);
 }
 
 }  // namespace
 
-size_t moe_workspace(int T, int topk, int I) {
-  return ((size_t)kRouteInts * 4 + 255) / 256 * 256 + (size_t)T * topk * I * sizeof(float);
-}
+size_t moe_workspace(int T, int topk, int I) { return kErrBytes + (size_t)T * topk * I * sizeof(float); }
 
 cudaError_t launch_moe(const void* x, long long ldx, const float* logits, long long ldl, int T, int E, int topk,
                        int renorm, int H, int I, const uint8_t* w13, const float* s13, const uint8_t* w2,
@@ -642,15 +713,13 @@ cudaError_t launch_moe(const void* x, long long ldx, const float* logits, long l
   MoeArgs a;
   a.x = static_cast<const __nv_bfloat16*>(x);
   a.logits = logits;
-  a.w13 = w13;
   a.s13 = s13;
-  a.w2 = w2;
   a.s2 = s2;
   a.y = static_cast<__nv_bfloat16*>(y);
   a.ids = ids;
   a.weights = weights;
-  a.route = static_cast<int*>(ws);
-  a.h = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + ((size_t)kRouteInts * 4 + 255) / 256 * 256);
+  a.err = static_cast<int*>(ws);
+  a.h = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kErrBytes);
   a.ldx = ldx;
   a.ldl = ldl;
   a.ldy = ldy;
@@ -660,25 +729,8 @@ cudaError_t launch_moe(const void* x, long long ldx, const float* logits, long l
   a.H = H;
   a.I = I;
   a.renorm = renorm;
-  static bool up_done[64] = {}, down_done[64] = {};
-  cudaError_t e = opt_in_smem((const void*)moe_gate_up_kernel, UpSmem::kBytes, up_done);
-  if (e == cudaSuccess)
-    e = opt_in_smem((const void*)moe_down_kernel, DownSmem::bytes(kMoeMaxTokens), down_done);
-  if (e != cudaSuccess) return e;
-  // as many CTAs as reside at once, or one per column group if that is less
-  const long long most = (long long)T * topk * (I / 8);
-  const long long grid = most < dev->sms * 2 ? most : dev->sms * 2;
-  void* up_args[] = {&a};
-  e = launch_pdl((const void*)moe_gate_up_kernel, dim3((unsigned)grid), dim3(kMoeThreads), UpSmem::kBytes, 1, stream,
-                 up_args);
-  if (e != cudaSuccess) return e;
-  // the widest cluster with which every CTA has an SM of its own
-  const int row_tiles = (H + kDownRows - 1) / kDownRows;
-  int C = 8;
-  while (C > 1 && row_tiles * C > dev->sms) C /= 2;
-  void* down_args[] = {&a, &C};
-  return launch_pdl((const void*)moe_down_kernel, dim3((unsigned)(row_tiles * C)), dim3(kMoeThreads),
-                    DownSmem::bytes(T), C, stream, down_args);
+  return T <= kSmallGroup ? launch_form<kSmallGroup>(a, w13, w2, dev, stream)
+                          : launch_form<kGroup>(a, w13, w2, dev, stream);
 }
 
 }  // namespace fp8

@@ -216,7 +216,7 @@ class Fp8Act:
 
 
 class Fp8Workspace:
-    """Zeroed workspace of fp8_linear (its error word) or fp8_moe (routing and
+    """Zeroed workspace of fp8_linear (its error word) or fp8_moe (error word and
     intermediate).  Calls that may run at the same time need one each."""
 
     def __init__(self, nbytes, device="cuda", stream=None):
@@ -241,7 +241,7 @@ class Fp8Workspace:
         return cls(n, device, stream)
 
     def check(self, stream=None):
-        """Synchronises and returns the error word of fp8_linear (0: none)."""
+        """Synchronises and returns the error word of the calls that used it (0: none)."""
         with _on(self.buf.device, stream) as s:
             return _sq.sharq_check_status(self.ptr, s)
 
