@@ -38,15 +38,24 @@ const Device* device() {
   return &d;
 }
 
-cudaError_t opt_in_smem(const void* kernel, int bytes, bool (&done)[64]) {
+namespace {
+cudaError_t set_once(const void* kernel, cudaFuncAttribute attr, int value, bool (&done)[64]) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
   if (done[dev]) return cudaSuccess;
-  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  e = cudaFuncSetAttribute(kernel, attr, value);
   if (e == cudaSuccess) done[dev] = true;
   return e;
+}
+}  // namespace
+
+cudaError_t opt_in_smem(const void* kernel, int bytes, bool (&done)[64]) {
+  return set_once(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes, done);
+}
+cudaError_t allow_wide_clusters(const void* kernel, bool (&done)[64]) {
+  return set_once(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1, done);
 }
 
 cudaError_t launch_pdl(const void* kernel, dim3 grid, dim3 block, int smem, int cluster, cudaStream_t stream,

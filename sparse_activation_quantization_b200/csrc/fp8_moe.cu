@@ -30,6 +30,8 @@
 // the logits by themselves: down does it, and fills its ring with weights, before
 // gate-up has ended.
 // No atomics touch results; the order of every sum follows from the routing.
+#include <cstddef>
+
 #include "fp8_skinny.cuh"
 
 namespace sharq {
@@ -53,6 +55,7 @@ struct MoeArgs {
   int* ids;                 // [T][topk] or nullptr
   float* weights;           // [T][topk] or nullptr
   int* err;                 // workspace: the error word
+  int* route;               // workspace: gate-up's routing, where down reads it
   float* h;                 // workspace: [T * topk][I]
   long long ldx, ldl, ldy;
   int T, E, topk, H, I, renorm;
@@ -64,19 +67,25 @@ struct MoeArgs {
 // calls of up to 8 tokens, whose groups never hold more.
 constexpr int kSmallGroup = 8, kGroup = 32;
 constexpr int kMaxGroups = kMoeMaxExperts + kMaxPairs / kGroup;
-struct Routing {
-  int n_groups;
-  short expert[kMaxGroups];  // ascending
-  short first[kMaxGroups];   // first of the group's pairs
-  short count[kMaxGroups];
-  short pairs[kMaxPairs];    // pair ids, expert by expert, by token
-  float p[kMaxPairs];        // by pair id
+struct Group {
+  short expert, first, count, form;  // first of its pairs, their number, tokens_form of it
 };
-struct RoutingScratch {
-  unsigned long long chose[kMoeMaxExperts];  // bit t: token t chose the expert
+struct Routing {
+  int n_groups, n_pairs;
+  float p[kMaxPairs];        // by pair id
+  short pairs[kMaxPairs];    // pair ids, expert by expert, by token
+  short token[kMaxPairs];    // their tokens
+  Group groups[kMaxGroups];  // experts ascending
+};
+constexpr int kRouteInts = (int)(sizeof(Routing) / 4);
+struct __align__(8) RoutingScratch {
+  uint32_t chose[2 * kMoeMaxExperts];  // two words an expert, bit t: token t chose it
   short first[kMoeMaxExperts];
   short expert_of[kMaxPairs];
 };
+
+// the form that takes a group of np tokens
+__device__ __forceinline__ int tokens_form(int np) { return np <= 8 ? 8 : (np <= 16 ? 16 : 32); }
 
 // Order-preserving key of a logit: larger logit, larger key; -0 equals +0; a
 // NaN sorts below everything, so an index is always valid.
@@ -96,63 +105,69 @@ __device__ __forceinline__ float logit_exp(float l, float mx) {
 }
 
 // The k largest logits of a token and their weights, a warp per token.  kPer:
-// logits per lane.
+// logits per lane.  A round is two warp reductions (the largest key, then the
+// lowest expert that has it) and no branch: about 100 cycles.
 template <int kPer>
 __device__ void choose_experts(const MoeArgs& a, Routing& r, RoutingScratch& sc, bool publish) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  for (int t = warp; t < a.T; t += kMoeWarps) {
+  float l[kPer];
+  auto fetch = [&](int t) {
     const float* lg = a.logits + (size_t)t * a.ldl;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) l[i] = t < a.T && lane + 32 * i < a.E ? __ldcg(lg + lane + 32 * i) : -INFINITY;
+  };
+  fetch(warp);
+  for (int t = warp; t < a.T; t += kMoeWarps) {
     uint32_t key[kPer];
-    float l[kPer], lmax = -INFINITY;
+    float cur[kPer];
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-      const int e = lane + 32 * i;
-      l[i] = e < a.E ? __ldcg(lg + e) : -INFINITY;
-      key[i] = e < a.E ? max(logit_key(l[i]), 1u) : 0u;  // 0: absent, or taken
-      if (l[i] > lmax) lmax = l[i];
+      cur[i] = l[i];
+      key[i] = lane + 32 * i < a.E ? max(logit_key(l[i]), 1u) : 0u;  // 0: absent, or taken
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) lmax = fmaxf(lmax, __shfl_xor_sync(0xffffffffu, lmax, o));
-    float sum = 0.0f;
-    if (!a.renorm) {
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) sum += logit_exp(l[i], lmax);
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    }
-    uint32_t my_key = 0u;
+    fetch(t + kMoeWarps);  // the next token's, while this one's rounds go on
+    uint32_t my_key = 0u, top = 0u, first = 0u;
     int my_e = 0;
     for (int j = 0; j < a.topk; ++j) {
-      uint32_t best = key[0];
-      int be = lane;
+      uint32_t k[kPer];
+      int at[kPer];
 #pragma unroll
-      for (int i = 1; i < kPer; ++i)
-        if (key[i] > best) {
-          best = key[i];
-          be = lane + 32 * i;
-        }
-      const uint32_t top = __reduce_max_sync(0xffffffffu, best);
-      const int e = __reduce_min_sync(0xffffffffu, best == top ? be : 0x7fffffff);
-#pragma unroll
-      for (int i = 0; i < kPer; ++i)
-        if (lane + 32 * i == e) key[i] = 0u;
-      if (lane == j) {
-        my_key = top;
-        my_e = e;
+      for (int i = 0; i < kPer; ++i) {
+        k[i] = key[i];
+        at[i] = lane + 32 * i;
       }
-    }
-    const float mine = lane < a.topk ? logit_exp(key_logit(my_key), lmax) : 0.0f;
-    if (a.renorm) {
-      sum = mine;
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      for (int w = 1; w < kPer; w *= 2)  // equal keys: the lower expert stays
+#pragma unroll
+        for (int i = 0; i + w < kPer; i += 2 * w) {
+          const bool up = k[i + w] > k[i];
+          k[i] = up ? k[i + w] : k[i];
+          at[i] = up ? at[i + w] : at[i];
+        }
+      top = __reduce_max_sync(0xffffffffu, k[0]);
+      const int e = __reduce_min_sync(0xffffffffu, k[0] == top ? at[0] : 0x7fffffff);
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) key[i] = lane + 32 * i == e ? 0u : key[i];
+      if (j == 0) first = top;
+      my_key = lane == j ? top : my_key;
+      my_e = lane == j ? e : my_e;
     }
+    const float lmax = key_logit(first);
+    const float mine = lane < a.topk ? logit_exp(key_logit(my_key), lmax) : 0.0f;
+    float sum = mine;
+    if (!a.renorm) {
+      sum = 0.0f;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) sum += logit_exp(cur[i], lmax);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     if (lane < a.topk) {
       const int pr = t * a.topk + lane;
       const float p = sum > 0.0f ? __fdiv_rn(mine, sum) : 0.0f;  // no logit above -inf: no expert counts
       r.p[pr] = p;
       sc.expert_of[pr] = p > 0.0f ? (short)my_e : (short)-1;  // weight 0: the expert is not evaluated
-      if (p > 0.0f) atomicOr(&sc.chose[my_e], 1ull << t);
+      if (p > 0.0f) atomicOr(&sc.chose[2 * my_e + (t >> 5)], 1u << (t & 31));
       if (publish) {
         if (a.ids) a.ids[pr] = my_e;
         if (a.weights) a.weights[pr] = p;
@@ -161,10 +176,14 @@ __device__ void choose_experts(const MoeArgs& a, Routing& r, RoutingScratch& sc,
   }
 }
 
-// Every CTA derives the same routing.  Ends with a barrier.
+__device__ __forceinline__ unsigned long long tokens_of(const RoutingScratch& sc, int e) {
+  return *reinterpret_cast<const unsigned long long*>(&sc.chose[2 * e]);
+}
+
+// The whole routing from the logits.  Ends with a barrier.
 template <int G>
 __device__ void build_routing(const MoeArgs& a, Routing& r, RoutingScratch& sc, bool publish) {
-  for (int e = threadIdx.x; e < a.E; e += kMoeThreads) sc.chose[e] = 0ull;
+  for (int i = threadIdx.x; i < 2 * a.E; i += kMoeThreads) sc.chose[i] = 0u;
   __syncthreads();
   if (a.E <= 128)
     choose_experts<4>(a, r, sc, publish);
@@ -175,7 +194,7 @@ __device__ void build_routing(const MoeArgs& a, Routing& r, RoutingScratch& sc, 
     const int per = (a.E + 31) / 32, e0 = threadIdx.x * per, e1 = min(a.E, e0 + per);
     int sum = 0;  // pairs in the low half, groups in the high
     for (int e = e0; e < e1; ++e) {
-      const int c = __popcll(sc.chose[e]);
+      const int c = __popcll(tokens_of(sc, e));
       sum += c + ((c + G - 1) / G << 16);
     }
     int at = sum;
@@ -184,16 +203,18 @@ __device__ void build_routing(const MoeArgs& a, Routing& r, RoutingScratch& sc, 
       const int v = __shfl_up_sync(0xffffffffu, at, o);
       if ((int)threadIdx.x >= o) at += v;
     }
-    if (threadIdx.x == 31) r.n_groups = at >> 16;
+    if (threadIdx.x == 31) {
+      r.n_groups = at >> 16;
+      r.n_pairs = at & 0xffff;
+    }
     at -= sum;
     int np = at & 0xffff, ng = at >> 16;
     for (int e = e0; e < e1; ++e) {
-      const int c = __popcll(sc.chose[e]);
+      const int c = __popcll(tokens_of(sc, e));
       sc.first[e] = (short)np;
       for (int i = 0; i < c; i += G) {
-        r.expert[ng] = (short)e;
-        r.first[ng] = (short)(np + i);
-        r.count[ng++] = (short)min(G, c - i);
+        const int n = min(G, c - i);
+        r.groups[ng++] = Group{(short)e, (short)(np + i), (short)n, (short)tokens_form(n)};
       }
       np += c;
     }
@@ -201,9 +222,41 @@ __device__ void build_routing(const MoeArgs& a, Routing& r, RoutingScratch& sc, 
   __syncthreads();
   for (int i = threadIdx.x; i < a.T * a.topk; i += kMoeThreads) {
     const int e = sc.expert_of[i], t = i / a.topk;
-    if (e >= 0) r.pairs[sc.first[e] + __popcll(sc.chose[e] & ((1ull << t) - 1))] = (short)i;
+    if (e >= 0) {
+      const int at = sc.first[e] + __popcll(tokens_of(sc, e) & ((1ull << t) - 1));
+      r.pairs[at] = (short)i;
+      r.token[at] = (short)t;
+    }
   }
   __syncthreads();
+}
+
+// The used parts of a routing to or from global memory, all threads.  Where the
+// parts end is known from the call alone, so every load is on its way at once.
+template <bool kRead>
+__device__ __forceinline__ void copy_routing(const MoeArgs& a, Routing& r, int* g) {
+  int* s = reinterpret_cast<int*>(&r);
+  const int pairs = a.T * a.topk, groups = min(pairs, kMaxGroups);
+  auto part = [&](size_t at, int n) {
+    const int w0 = (int)(at / 4);
+    for (int i0 = 0; i0 < n; i0 += 4 * kMoeThreads) {
+      int v[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int i = i0 + j * kMoeThreads + (int)threadIdx.x;
+        if (i < n) v[j] = kRead ? __ldcg(g + w0 + i) : s[w0 + i];
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int i = i0 + j * kMoeThreads + (int)threadIdx.x;
+        if (i < n) (kRead ? s : g)[w0 + i] = v[j];
+      }
+    }
+  };
+  part(0, 2 + pairs);                                                    // counts and p
+  part(offsetof(Routing, pairs), (pairs + 1) / 2);
+  part(offsetof(Routing, token), (pairs + 1) / 2);
+  part(offsetof(Routing, groups), groups * (int)(sizeof(Group) / 4));
 }
 
 // ------------------------------------------------------ columns on the fly ---
@@ -233,61 +286,76 @@ struct Raw8 {
 };
 
 // Block b of np tokens into a stage's B operand (128-byte swizzle) and scales, by
-// one warp: half a warp per token, eight values a lane.  rows(n): token n's row.
+// one warp: half a warp per token, eight values a lane, kBatch tokens of each half
+// side by side.  rows(n): token n's row; weights(n): a factor of its scale.
 // Columns of no token keep what they held: their sums are not used.
-template <int J, class T, class Rows>
-__device__ __forceinline__ void form_columns(uint8_t* dst, float* scale, int np, int P, int b, int K, Rows rows) {
+template <int J, class T, int kBatch, class Rows, class Weights>
+__device__ __forceinline__ void form_batch(uint8_t* dst, float* scale, int n0, int np, int P, int b, int K, Rows rows,
+                                           Weights weights) {
   const int lane = threadIdx.x & 31, l16 = lane & 15, half = lane >> 4;
   const int k = b * kBlock + l16 * 8;
-  constexpr int kBatch = 4;  // loads in flight per lane
-  for (int n0 = 0; n0 < np; n0 += 2 * kBatch) {
-    Raw8<T> raw[kBatch];  // every load is on its way before the first value is used
+  Raw8<T> raw[kBatch];  // every load is on its way before the first value is used
+#pragma unroll
+  for (int i = 0; i < kBatch; ++i) {
+    const int n = n0 + 2 * i + half;
+    raw[i].clear();
+    if (n < np && k < K) raw[i].load(static_cast<const T*>(rows(n)) + k);
+  }
+  float f[kBatch][8], m[kBatch];
+#pragma unroll
+  for (int i = 0; i < kBatch; ++i) {
+    raw[i].floats(f[i]);
+    m[i] = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) m[i] = fmaxf(m[i], fabsf(f[i][e]));
+  }
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1)
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) m[i] = fmaxf(m[i], __shfl_xor_sync(0xffffffffu, m[i], o));
+#pragma unroll
+  for (int i = 0; i < kBatch; ++i) {
+    const int n = n0 + 2 * i + half;
+    // 2^(7 - floor(log2 m)) from the exponent field; the clamp keeps it and its inverse normal numbers
+    const uint32_t ef = max(__float_as_uint(m[i]) >> 23, 20u);
+    const float up = __uint_as_float((261u - ef) << 23);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[i][e] *= up;
+    if (n < np && l16 == 0)  // an infinity saturates in E4M3: it is in the scale
+      scale[n] = (ef == 255u ? INFINITY : __uint_as_float((ef - 7u) << 23)) * weights(n);
+  }
+#pragma unroll
+  for (int j = 0; j < J; ++j)
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
       const int n = n0 + 2 * i + half;
-      raw[i].clear();
-      if (n < np && k < K) raw[i].load(static_cast<const T*>(rows(n)) + k);
-    }
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      const int n = n0 + 2 * i + half;
-      if (n0 + 2 * i >= np) break;  // uniform over the warp
-      float f[8];
-      raw[i].floats(f);
-      float m = 0.0f;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(f[e]));
-#pragma unroll
-      for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-      // 2^(7 - floor(log2 m)) from the exponent field; the clamp keeps it and its inverse normal numbers
-      const uint32_t ef = max(__float_as_uint(m) >> 23, 20u);
-      const float up = __uint_as_float((261u - ef) << 23);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) f[e] *= up;
-      if (n < np && l16 == 0)  // an infinity saturates in E4M3: it is in the scale
-        scale[n] = ef == 255u ? INFINITY : __uint_as_float((ef - 7u) << 23);
-#pragma unroll
-      for (int j = 0; j < J; ++j) {
-        const uint32_t c0 = e4m3x4(f[0], f[1], f[2], f[3]), c1 = e4m3x4(f[4], f[5], f[6], f[7]);
-        if (n < np) {
-          const uint32_t row = (uint32_t)(j * P + n);
-          *reinterpret_cast<uint2*>(dst + codes_chunk_off(row, l16 >> 1) + (l16 & 1) * 8) = make_uint2(c0, c1);
-        }
-        if (j + 1 < J) {
-          const float2 d0 = e4m3x2_to_float(c0), d1 = e4m3x2_to_float(c0 >> 16);
-          const float2 d2 = e4m3x2_to_float(c1), d3 = e4m3x2_to_float(c1 >> 16);
-          f[0] = (f[0] - d0.x) * 16.0f, f[1] = (f[1] - d0.y) * 16.0f;
-          f[2] = (f[2] - d1.x) * 16.0f, f[3] = (f[3] - d1.y) * 16.0f;
-          f[4] = (f[4] - d2.x) * 16.0f, f[5] = (f[5] - d2.y) * 16.0f;
-          f[6] = (f[6] - d3.x) * 16.0f, f[7] = (f[7] - d3.y) * 16.0f;
-        }
+      float(&v)[8] = f[i];
+      const uint32_t c0 = e4m3x4(v[0], v[1], v[2], v[3]), c1 = e4m3x4(v[4], v[5], v[6], v[7]);
+      if (n < np)
+        *reinterpret_cast<uint2*>(dst + codes_chunk_off((uint32_t)(j * P + n), l16 >> 1) + (l16 & 1) * 8) =
+            make_uint2(c0, c1);
+      if (j + 1 < J) {
+        const float2 d0 = e4m3x2_to_float(c0), d1 = e4m3x2_to_float(c0 >> 16);
+        const float2 d2 = e4m3x2_to_float(c1), d3 = e4m3x2_to_float(c1 >> 16);
+        v[0] = (v[0] - d0.x) * 16.0f, v[1] = (v[1] - d0.y) * 16.0f;
+        v[2] = (v[2] - d1.x) * 16.0f, v[3] = (v[3] - d1.y) * 16.0f;
+        v[4] = (v[4] - d2.x) * 16.0f, v[5] = (v[5] - d2.y) * 16.0f;
+        v[6] = (v[6] - d3.x) * 16.0f, v[7] = (v[7] - d3.y) * 16.0f;
       }
     }
-  }
+}
+template <int J, class T, class Rows, class Weights>
+__device__ __forceinline__ void form_columns(uint8_t* dst, float* scale, int np, int P, int b, int K, Rows rows,
+                                             Weights weights) {
+  int n0 = 0;
+  for (; np - n0 > 4; n0 += 8) form_batch<J, T, 4>(dst, scale, n0, np, P, b, K, rows, weights);
+  if (np - n0 > 2)
+    form_batch<J, T, 2>(dst, scale, n0, np, P, b, K, rows, weights);
+  else if (np > n0)
+    form_batch<J, T, 1>(dst, scale, n0, np, P, b, K, rows, weights);
 }
 
 __host__ __device__ constexpr int mma_n(int cols) { return (cols + 15) / 16 * 16; }
-__device__ __forceinline__ int tokens_form(int np) { return np <= 8 ? 8 : (np <= 16 ? 16 : 32); }
 
 // One finished unit's sums: acc[t] += (c1 + c2 / 16 (+ c3 / 256)) scale[t] s_w
 template <int J, int P, int kStages>
@@ -322,6 +390,10 @@ struct MoeRing {
   static constexpr int kStageBytes = kUnitBytes + kCols * kBlock;
   static constexpr int kTmem = tmem_cols(kCols * kStages);
   static constexpr int kBytes = kStages * kStageBytes;
+  // Warps that form columns, a unit each in turn.  Never more than stages: a warp that comes to unit i has formed
+  // unit i - kFormers, so every stage up to unit i - kFormers - kStages has been emptied, and the parity that it
+  // waits for (unit i - kStages) can only be the next to come, not one two uses back.
+  static constexpr int kFormers = kFormWarps < kStages ? kFormWarps : kStages;
   static_assert(kTmem <= 512 && kStageBytes % 1024 == 0, "ring");
 };
 
@@ -379,6 +451,7 @@ __global__ void __launch_bounds__(kMoeThreads, G == kSmallGroup ? 2 : 1)
   const uint32_t tmem = bars.tmem;
   pdl_wait();
   build_routing<G>(a, r, *reinterpret_cast<RoutingScratch*>(smem), blockIdx.x == 0);
+  if (blockIdx.x == 0 && a.route) copy_routing<false>(a, r, a.route);
   pdl_trigger();  // after the allocation, and after the logits of the kernels before are complete
   const int nkb = blocks_of(a.H), tiles = (a.I + kUpCols - 1) / kUpCols, items = r.n_groups * tiles;
   const int S = a.splits, rank = S > 1 ? (int)cluster_ctarank() : 0;
@@ -394,7 +467,7 @@ __global__ void __launch_bounds__(kMoeThreads, G == kSmallGroup ? 2 : 1)
       Pos p;
       int n = 0;
       for (int it = it0; it < it1 && !bars.abort; ++it) {
-        const int grp = it / tiles, i0 = (it - grp * tiles) * kUpCols, e = r.expert[grp];
+        const int grp = it / tiles, i0 = (it - grp * tiles) * kUpCols, e = r.groups[grp].expert;
         for (int b = b0; b < b1; ++b, ++n, p.next()) {
           if (!wait_empty(bars, p, deadline)) {
             bars.give_up(a.err);
@@ -413,7 +486,7 @@ __global__ void __launch_bounds__(kMoeThreads, G == kSmallGroup ? 2 : 1)
     if (elect_one()) {
       Pos p;
       for (int it = it0; it < it1 && !bars.abort; ++it) {
-        const uint32_t idesc = idesc_e4m3(kUnitRows, mma_n(kUpTerms * tokens_form(r.count[it / tiles])));
+        const uint32_t idesc = idesc_e4m3(kUnitRows, mma_n(kUpTerms * r.groups[it / tiles].form));
         for (int b = b0; b < b1; ++b, p.next()) {
           if (!mbar_wait(&bars.full[p.s], p.phase, deadline, &bars.abort)) {
             bars.give_up(a.err);
@@ -427,18 +500,20 @@ __global__ void __launch_bounds__(kMoeThreads, G == kSmallGroup ? 2 : 1)
     }
   } else if (warp >= kFirstFormWarp) {
     Pos p;
+    static_assert(C::kFormers == kFormWarps, "every former has a turn");
     int turn = warp - kFirstFormWarp;  // units until this warp's next
     for (int it = it0; it < it1 && !bars.abort; ++it) {
-      const int grp = it / tiles, np = r.count[grp], p0 = r.first[grp], P = tokens_form(np);
+      const Group gr = r.groups[it / tiles];
       for (int b = b0; b < b1; ++b, p.next()) {
         if (turn-- > 0) continue;
-        turn = kFormWarps - 1;
+        turn = C::kFormers - 1;
         if (!__all_sync(0xffffffffu, wait_empty(bars, p, deadline))) {
           bars.give_up(a.err);
           break;
         }
-        form_columns<kUpTerms, __nv_bfloat16>(smem + p.s * C::kStageBytes + kUnitBytes, scale[p.s], np, P, b, a.H,
-                                              [&](int n) { return a.x + (size_t)(r.pairs[p0 + n] / a.topk) * a.ldx; });
+        form_columns<kUpTerms, __nv_bfloat16>(
+            smem + p.s * C::kStageBytes + kUnitBytes, scale[p.s], gr.count, gr.form, b, a.H,
+            [&](int n) { return a.x + (size_t)r.token[gr.first + n] * a.ldx; }, [](int) { return 1.0f; });
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive_cta(&bars.full[p.s]);
@@ -450,9 +525,9 @@ __global__ void __launch_bounds__(kMoeThreads, G == kSmallGroup ? 2 : 1)
     const uint32_t tmem_lane = tmem + ((uint32_t)(warp * 32) << 16);
     for (int it = it0; it < it1 && !bars.abort; ++it) {
       const int grp = it / tiles, c0 = (it - grp * tiles) * kUpCols + 16 * warp;
-      const int np = r.count[grp], p0 = r.first[grp];
+      const int np = r.groups[grp].count, p0 = r.groups[grp].first;
       // the warp's 16 gate rows lie in one scale block, its up rows in another; rows past the last read zeros
-      const float* s13 = a.s13 + (size_t)r.expert[grp] * rb * nkb;
+      const float* s13 = a.s13 + (size_t)r.groups[grp].expert * rb * nkb;
       const int row = min(c0, a.I - 16);
       ScaleRow sg, su;
       sg.start(s13 + (size_t)(row / kBlock) * nkb, nkb, b0, lane);
@@ -497,7 +572,8 @@ __global__ void __launch_bounds__(kMoeThreads, G == kSmallGroup ? 2 : 1)
   if (S > 1) {
     cluster_sync_all();  // every CTA's sums are in its shared memory
     if (it0 < it1 && !bars.abort) {
-      const int grp = it0 / tiles, i0 = (it0 - grp * tiles) * kUpCols, np = r.count[grp], p0 = r.first[grp];
+      const int grp = it0 / tiles, i0 = (it0 - grp * tiles) * kUpCols;
+      const int np = r.groups[grp].count, p0 = r.groups[grp].first;
       const uint32_t base = smem_u32(smem);
       const int total = np * kUpCols;
       for (int i = rank * total / S + (int)threadIdx.x; i < (rank + 1) * total / S; i += kMoeThreads) {
@@ -520,18 +596,22 @@ __global__ void __launch_bounds__(kMoeThreads, G == kSmallGroup ? 2 : 1)
 // ------------------------------------------------------------------- down ---
 
 constexpr int kDownTerms = 3;
-template <int G>
-struct Down : MoeRing<kDownTerms, G, G == kSmallGroup ? 4 : 5> {
+// kEarly, for calls whose CTAs fit an SM beside gate-up's: derive the routing and
+// fill the ring with weights before gate-up has ended.  Otherwise gate-up's routing
+// is read once it has.
+template <int G, bool kEarly>
+struct Down : MoeRing<kDownTerms, G, kEarly ? 4 : (G == kSmallGroup ? 3 : 5)> {
   static constexpr int kSums = Down::kBytes;  // [T][128]
   static constexpr int bytes(int T) { return kSums + T * kUnitRows * 4 + 1024; }
 };
-static_assert(Up<kSmallGroup>::kSmemBytes + Down<kSmallGroup>::bytes(kSmallGroup) + 2 * (int)sizeof(Routing) <= 226 * 1024 &&
-              Up<kSmallGroup>::kTmem + Down<kSmallGroup>::kTmem <= 512, "both kernels' small forms share an SM");
+using EarlyDown = Down<kSmallGroup, true>;
+static_assert(Up<kSmallGroup>::kSmemBytes + EarlyDown::bytes(kSmallGroup) + 2 * (int)sizeof(Routing) <= 226 * 1024 &&
+              Up<kSmallGroup>::kTmem + EarlyDown::kTmem <= 512, "both kernels' forms share an SM");
 
-template <int G>
+template <int G, bool kEarly>
 __global__ void __launch_bounds__(kMoeThreads, G == kSmallGroup ? 2 : 1)
     moe_down_kernel(const __grid_constant__ CUtensorMap map, const MoeArgs a) {
-  using C = Down<G>;
+  using C = Down<G, kEarly>;
   using Pos = RingPos<C::kStages>;
   extern __shared__ uint8_t smem_raw[];
   __shared__ Routing r;
@@ -546,8 +626,13 @@ __global__ void __launch_bounds__(kMoeThreads, G == kSmallGroup ? 2 : 1)
   moe_setup<C>(bars, &map);
   const uint32_t tmem = bars.tmem;
   pdl_trigger();  // after the allocation
-  // Logits and weights: complete before gate-up let this grid start.
-  build_routing<G>(a, r, *reinterpret_cast<RoutingScratch*>(smem), false);
+  if (kEarly) {  // logits and weights were complete before gate-up let this grid start
+    build_routing<G>(a, r, *reinterpret_cast<RoutingScratch*>(smem), false);
+  } else {
+    pdl_wait();
+    copy_routing<true>(a, r, a.route);
+    __syncthreads();
+  }
   for (int i = threadIdx.x; i < a.T * kUnitRows; i += kMoeThreads) sums[i] = 0.0f;
   const int units = r.n_groups * nkb;
   const int u0 = (int)((long long)rank * units / S), u1 = (int)((long long)(rank + 1) * units / S);
@@ -565,7 +650,7 @@ __global__ void __launch_bounds__(kMoeThreads, G == kSmallGroup ? 2 : 1)
           break;
         }
         mbar_arrive_expect_tx(&bars.full[p.s], kUnitBytes);
-        tma_2d(smem + p.s * C::kStageBytes, &map, b * kBlock, r.expert[grp] * a.H + d0, &bars.full[p.s]);
+        tma_2d(smem + p.s * C::kStageBytes, &map, b * kBlock, r.groups[grp].expert * a.H + d0, &bars.full[p.s]);
         if (++b == nkb) {
           b = 0;
           ++grp;
@@ -577,7 +662,7 @@ __global__ void __launch_bounds__(kMoeThreads, G == kSmallGroup ? 2 : 1)
     if (elect_one()) {
       Pos p;
       for (int u = u0; u < u1; ++u, p.next()) {
-        const uint32_t idesc = idesc_e4m3(kUnitRows, mma_n(kDownTerms * tokens_form(r.count[u / nkb])));
+        const uint32_t idesc = idesc_e4m3(kUnitRows, mma_n(kDownTerms * r.groups[u / nkb].form));
         if (!mbar_wait(&bars.full[p.s], p.phase, deadline, &bars.abort)) {
           bars.give_up(a.err);
           break;
@@ -591,14 +676,17 @@ __global__ void __launch_bounds__(kMoeThreads, G == kSmallGroup ? 2 : 1)
     pdl_wait();  // gate-up has ended: h is complete
     Pos p;
     for (int u = u0; u < u1; ++u, p.next()) {
-      if ((u - u0) % kFormWarps != warp - kFirstFormWarp) continue;
-      const int grp = u / nkb, np = r.count[grp], p0 = r.first[grp];
+      if ((u - u0) % C::kFormers != warp - kFirstFormWarp) continue;
+      const int grp = u / nkb;
+      const Group gr = r.groups[grp];
       if (!__all_sync(0xffffffffu, wait_empty(bars, p, deadline))) {
         bars.give_up(a.err);
         break;
       }
-      form_columns<kDownTerms, float>(smem + p.s * C::kStageBytes + kUnitBytes, scale[p.s], np, tokens_form(np),
-                                      u - grp * nkb, a.I, [&](int n) { return a.h + (size_t)r.pairs[p0 + n] * a.I; });
+      form_columns<kDownTerms, float>(
+          smem + p.s * C::kStageBytes + kUnitBytes, scale[p.s], gr.count, gr.form, u - grp * nkb, a.I,
+          [&](int n) { return a.h + (size_t)r.pairs[gr.first + n] * a.I; },
+          [&](int n) { return r.p[r.pairs[gr.first + n]]; });
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive_cta(&bars.full[p.s]);
@@ -606,11 +694,18 @@ __global__ void __launch_bounds__(kMoeThreads, G == kSmallGroup ? 2 : 1)
   } else {
     Pos p;
     const uint32_t tmem_lane = tmem + ((uint32_t)(warp * 32) << 16);
+    auto scales_of = [&](int grp, int b) {
+      ScaleRow w;
+      w.start(a.s2 + ((size_t)r.groups[grp].expert * rb + d0 / kBlock) * nkb, nkb, b, lane);
+      return w;
+    };
+    ScaleRow ahead;
+    if (u0 < u1) ahead = scales_of(u0 / nkb, u0 % nkb);
     for (int u = u0; u < u1 && !bars.abort;) {
       const int grp = u / nkb, bb = u - grp * nkb, be = min(nkb, bb + u1 - u);
-      const int np = r.count[grp], p0 = r.first[grp];
-      ScaleRow sw;
-      sw.start(a.s2 + ((size_t)r.expert[grp] * rb + d0 / kBlock) * nkb, nkb, bb, lane);
+      const int np = r.groups[grp].count, p0 = r.groups[grp].first;
+      ScaleRow sw = ahead;
+      if (grp + 1 < r.n_groups) ahead = scales_of(grp + 1, 0);  // read while this group is summed
       auto run = [&](auto form) {
         constexpr int P = decltype(form)::value;
         float acc[P] = {};
@@ -621,14 +716,22 @@ __global__ void __launch_bounds__(kMoeThreads, G == kSmallGroup ? 2 : 1)
             return;
           }
         }
-        // this thread alone adds to its row's sums; an expert appears once in a token's choices
+        // This thread alone adds to its row's sums, and a group's tokens are different ones: an expert appears
+        // once in a token's choices.
 #pragma unroll
-        for (int n = 0; n < P; ++n)
-          if (n < np) {
-            const int pc = r.pairs[p0 + n];
-            float* dst = sums + (size_t)(pc / a.topk) * kUnitRows + threadIdx.x;
-            *dst = fmaf(r.p[pc], acc[n], *dst);
-          }
+        for (int n0 = 0; n0 < P; n0 += 8) {
+          float* at[8];
+          float old[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (n0 + i < np) {
+              at[i] = sums + (size_t)r.token[p0 + n0 + i] * kUnitRows + threadIdx.x;
+              old[i] = *at[i];
+            }
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (n0 + i < np) *at[i] = old[i] + acc[n0 + i];
+        }
       };
       if (np <= 8)
         run(Tokens<8>{});
@@ -664,20 +767,25 @@ __global__ void __launch_bounds__(kMoeThreads, G == kSmallGroup ? 2 : 1)
   moe_teardown<C>(tmem);
 }
 
-constexpr size_t kErrBytes = 256;
+constexpr int kMaxCluster = 16;
+constexpr size_t kErrBytes = 256, kRouteBytes = (sizeof(Routing) + 255) / 256 * 256;
 
-template <int G>
+template <int G, bool kEarly>
 cudaError_t launch_form(MoeArgs& a, const uint8_t* w13, const uint8_t* w2, const Device* dev, cudaStream_t stream) {
   using U = Up<G>;
-  using D = Down<G>;
+  using D = Down<G, kEarly>;
   CUtensorMap m13, m2;
   if (!halves_map(&m13, w13, (uint64_t)a.E, (uint64_t)a.I, (uint64_t)a.H, 16) ||
       !byte_map(&m2, w2, (uint64_t)a.E * a.H, (uint64_t)a.I, kUnitRows))
     return cudaErrorInvalidValue;
   static bool up_done[64] = {}, down_done[64] = {};
-  cudaError_t e = opt_in_smem((const void*)moe_gate_up_kernel<G>, U::kSmemBytes, up_done);
-  if (e == cudaSuccess) e = opt_in_smem((const void*)moe_down_kernel<G>, D::bytes(G == kSmallGroup ? G : kMoeMaxTokens), down_done);
+  const void *up = (const void*)moe_gate_up_kernel<G>, *down = (const void*)moe_down_kernel<G, kEarly>;
+  cudaError_t e = opt_in_smem(up, U::kSmemBytes, up_done);
+  if (e == cudaSuccess) e = opt_in_smem(down, D::bytes(kEarly ? G : kMoeMaxTokens), down_done);
   if (e != cudaSuccess) return e;
+  static bool wide_done[64] = {};
+  if ((e = allow_wide_clusters(down, wide_done)) != cudaSuccess) return e;
+  if (kEarly) a.route = nullptr;
   // Items if every choice were another expert; with few, clusters share them.
   // Otherwise as many CTAs as reside at once.
   const int pairs = a.T * a.topk, tiles = (a.I + kUpCols - 1) / kUpCols;
@@ -687,21 +795,23 @@ cudaError_t launch_form(MoeArgs& a, const uint8_t* w13, const uint8_t* w2, const
   while (a.splits < 8 && 2 * a.splits <= nkb && 2 * a.splits * most <= dev->sms) a.splits *= 2;
   const int resident = dev->sms * (G == kSmallGroup ? 2 : 1);
   void* up_args[] = {&m13, &a};
-  e = launch_pdl((const void*)moe_gate_up_kernel<G>, dim3((unsigned)((most < resident ? most : resident) * a.splits)),
+  e = launch_pdl(up, dim3((unsigned)((most < resident ? most : resident) * a.splits)),
                  dim3(kMoeThreads), U::kSmemBytes, a.splits, stream, up_args);
   if (e != cudaSuccess) return e;
-  // the widest cluster with which every CTA has an SM of its own
+  // the widest cluster with which every CTA resides at once
   const int row_tiles = (a.H + kUnitRows - 1) / kUnitRows;
-  a.splits = 8;
-  while (a.splits > 1 && row_tiles * a.splits > dev->sms) a.splits /= 2;
+  a.splits = kMaxCluster;
+  while (a.splits > 1 && row_tiles * a.splits > (kEarly ? dev->sms : resident)) a.splits /= 2;
   void* down_args[] = {&m2, &a};
-  return launch_pdl((const void*)moe_down_kernel<G>, dim3((unsigned)(row_tiles * a.splits)), dim3(kMoeThreads),
+  return launch_pdl(down, dim3((unsigned)(row_tiles * a.splits)), dim3(kMoeThreads),
                     D::bytes(a.T), a.splits, stream, down_args);
 }
 
 }  // namespace
 
-size_t moe_workspace(int T, int topk, int I) { return kErrBytes + (size_t)T * topk * I * sizeof(float); }
+size_t moe_workspace(int T, int topk, int I) {
+  return kErrBytes + kRouteBytes + (size_t)T * topk * I * sizeof(float);
+}
 
 cudaError_t launch_moe(const void* x, long long ldx, const float* logits, long long ldl, int T, int E, int topk,
                        int renorm, int H, int I, const uint8_t* w13, const float* s13, const uint8_t* w2,
@@ -719,7 +829,8 @@ cudaError_t launch_moe(const void* x, long long ldx, const float* logits, long l
   a.ids = ids;
   a.weights = weights;
   a.err = static_cast<int*>(ws);
-  a.h = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kErrBytes);
+  a.route = reinterpret_cast<int*>(static_cast<uint8_t*>(ws) + kErrBytes);
+  a.h = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kErrBytes + kRouteBytes);
   a.ldx = ldx;
   a.ldl = ldl;
   a.ldy = ldy;
@@ -729,8 +840,11 @@ cudaError_t launch_moe(const void* x, long long ldx, const float* logits, long l
   a.H = H;
   a.I = I;
   a.renorm = renorm;
-  return T <= kSmallGroup ? launch_form<kSmallGroup>(a, w13, w2, dev, stream)
-                          : launch_form<kGroup>(a, w13, w2, dev, stream);
+  if (T <= kSmallGroup) return launch_form<kSmallGroup, true>(a, w13, w2, dev, stream);
+  // Groups of 8 while an expert has 4 tokens on average: two gate-up CTAs reside on an SM, and the few experts with
+  // more than 8 tokens are read again from L2.
+  if (T * topk <= 4 * E) return launch_form<kSmallGroup, false>(a, w13, w2, dev, stream);
+  return launch_form<kGroup, false>(a, w13, w2, dev, stream);
 }
 
 }  // namespace fp8
