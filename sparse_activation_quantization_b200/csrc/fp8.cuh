@@ -214,8 +214,6 @@ struct Device {
 const Device* device();
 // a kernel's attribute that is set once per device: `done` is the kernel's own table
 cudaError_t opt_in_smem(const void* kernel, int bytes, bool (&done)[64]);
-// clusters of more than 8 CTAs, likewise
-cudaError_t allow_wide_clusters(const void* kernel, bool (&done)[64]);
 // launch with programmatic dependence on the preceding kernel, and a cluster along x
 cudaError_t launch_pdl(const void* kernel, dim3 grid, dim3 block, int smem, int cluster, cudaStream_t stream,
                        void** args);

@@ -13,7 +13,7 @@ cudaError_t launch_prep(int kind, const void* x, long long ldx, const void* b, l
 cudaError_t launch_pack(const void* W, int K, int D, int E, uint8_t* codes, float* scales, cudaStream_t stream);
 cudaError_t launch_linear(const uint8_t* x, const float* xs, int lds, int T, int K, const uint8_t* w, const float* ws,
                           int D, void* y, long long ldy, int out_f32, int* err, cudaStream_t stream);
-size_t moe_workspace(int T, int topk, int I);
+size_t moe_workspace(int T, int topk, int H, int I);
 cudaError_t launch_moe(const void* x, long long ldx, const float* logits, long long ldl, int T, int E, int topk,
                        int renorm, int H, int I, const uint8_t* w13, const float* s13, const uint8_t* w2,
                        const float* s2, void* y, long long ldy, int* ids, float* weights, void* ws,
@@ -38,24 +38,15 @@ const Device* device() {
   return &d;
 }
 
-namespace {
-cudaError_t set_once(const void* kernel, cudaFuncAttribute attr, int value, bool (&done)[64]) {
+cudaError_t opt_in_smem(const void* kernel, int bytes, bool (&done)[64]) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
   if (done[dev]) return cudaSuccess;
-  e = cudaFuncSetAttribute(kernel, attr, value);
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e == cudaSuccess) done[dev] = true;
   return e;
-}
-}  // namespace
-
-cudaError_t opt_in_smem(const void* kernel, int bytes, bool (&done)[64]) {
-  return set_once(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes, done);
-}
-cudaError_t allow_wide_clusters(const void* kernel, bool (&done)[64]) {
-  return set_once(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1, done);
 }
 
 cudaError_t launch_pdl(const void* kernel, dim3 grid, dim3 block, int smem, int cluster, cudaStream_t stream,
@@ -290,7 +281,7 @@ size_t sharq_fp8_moe_workspace_bytes(int T, int topk, int H, int I, int E) {
   if (T < 0 || T > SHARQ_FP8_MOE_MAX_T || topk < 1 || topk > SHARQ_FP8_MOE_MAX_TOPK || topk > E || E < 1 ||
       E > SHARQ_FP8_MOE_MAX_E || !ok_k(H) || !ok_k(I))
     return 0;
-  return sharq::fp8::moe_workspace(T, topk, I);
+  return sharq::fp8::moe_workspace(T, topk, H, I);
 }
 
 int sharq_fp8_moe(const void* d_X, int64_t ldx, const float* d_logits, int64_t ldl, int T, int topk, int renormalize,

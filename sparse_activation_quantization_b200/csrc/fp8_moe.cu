@@ -1,4 +1,5 @@
-// fp8_moe.cu - a whole mixture-of-experts layer for a few tokens, two kernels.
+// fp8_moe.cu - a whole mixture-of-experts layer for a few tokens: two kernels, and
+// one that chooses the experts above 8 tokens.
 //
 //   chosen(t) = the k largest router logits of token t (ties: lower index)
 //   p(t, j)   = softmax of the logits over the chosen (or over all) experts
@@ -26,12 +27,11 @@
 //            token in shared memory; the CTAs' sums are joined in rank order over
 //            distributed shared memory.
 // Warps of a CTA: 0-3 sums, 4 copies (one thread), 5 MMAs (one thread) and TMEM,
-// 6-9 form the columns, a unit each in turn.  Both kernels derive the routing from
-// the logits by themselves: down does it, and fills its ring with weights, before
-// gate-up has ended.
+// 6-9 form the columns, a unit each in turn.  Up to 8 tokens every CTA chooses their
+// experts itself, a warp per token; above that a small kernel does it before (64
+// tokens on ten warps took 15 us of gate-up).  Down does not wait for gate-up to
+// derive the routing and to fill its ring with weights.
 // No atomics touch results; the order of every sum follows from the routing.
-#include <cstddef>
-
 #include "fp8_skinny.cuh"
 
 namespace sharq {
@@ -55,11 +55,15 @@ struct MoeArgs {
   int* ids;                 // [T][topk] or nullptr
   float* weights;           // [T][topk] or nullptr
   int* err;                 // workspace: the error word
-  int* route;               // workspace: gate-up's routing, where down reads it
+  int* choice;              // workspace: [T * topk] experts and weights of the choice kernel
+  float* choice_p;
+  int* arrived;             // workspace: down's arrivals [tile][8], zero between calls
+  float* partial;           // workspace: down's partial sums [tile][parts][T][128]
   float* h;                 // workspace: [T * topk][I]
   long long ldx, ldl, ldy;
   int T, E, topk, H, I, renorm;
   int splits;               // CTAs of a cluster
+  int parts;                // down: clusters that share a tile
 };
 
 // The routing in shared memory: per expert the (token, choice) pairs
@@ -77,7 +81,6 @@ struct Routing {
   short token[kMaxPairs];    // their tokens
   Group groups[kMaxGroups];  // experts ascending
 };
-constexpr int kRouteInts = (int)(sizeof(Routing) / 4);
 struct __align__(8) RoutingScratch {
   uint32_t chose[2 * kMoeMaxExperts];  // two words an expert, bit t: token t chose it
   short first[kMoeMaxExperts];
@@ -104,75 +107,85 @@ __device__ __forceinline__ float logit_exp(float l, float mx) {
   return l == mx ? 1.0f : expf(l - mx);
 }
 
-// The k largest logits of a token and their weights, a warp per token.  kPer:
-// logits per lane.  A round is two warp reductions (the largest key, then the
-// lowest expert that has it) and no branch: about 100 cycles.
+// The k largest logits of a token and their weights, by one warp: lane j < topk
+// gets the j-th.  kPer: logits per lane.  A round is two warp reductions (the
+// largest key, then the lowest expert that has it) and no branch: about 100
+// cycles.
 template <int kPer>
-__device__ void choose_experts(const MoeArgs& a, Routing& r, RoutingScratch& sc, bool publish) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+__device__ __forceinline__ void choose(const MoeArgs& a, int t, int& my_e, float& my_p) {
+  const int lane = threadIdx.x & 31;
+  const float* lg = a.logits + (size_t)t * a.ldl;
   float l[kPer];
-  auto fetch = [&](int t) {
-    const float* lg = a.logits + (size_t)t * a.ldl;
+  uint32_t key[kPer];
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) l[i] = t < a.T && lane + 32 * i < a.E ? __ldcg(lg + lane + 32 * i) : -INFINITY;
-  };
-  fetch(warp);
-  for (int t = warp; t < a.T; t += kMoeWarps) {
-    uint32_t key[kPer];
-    float cur[kPer];
+  for (int i = 0; i < kPer; ++i) l[i] = lane + 32 * i < a.E ? __ldcg(lg + lane + 32 * i) : -INFINITY;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) key[i] = lane + 32 * i < a.E ? max(logit_key(l[i]), 1u) : 0u;  // 0: absent, or taken
+  uint32_t my_key = 0u, first = 0u;
+  my_e = 0;
+  for (int j = 0; j < a.topk; ++j) {
+    uint32_t k[kPer];
+    int at[kPer];
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-      cur[i] = l[i];
-      key[i] = lane + 32 * i < a.E ? max(logit_key(l[i]), 1u) : 0u;  // 0: absent, or taken
+      k[i] = key[i];
+      at[i] = lane + 32 * i;
     }
-    fetch(t + kMoeWarps);  // the next token's, while this one's rounds go on
-    uint32_t my_key = 0u, top = 0u, first = 0u;
-    int my_e = 0;
-    for (int j = 0; j < a.topk; ++j) {
-      uint32_t k[kPer];
-      int at[kPer];
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        k[i] = key[i];
-        at[i] = lane + 32 * i;
+    for (int w = 1; w < kPer; w *= 2)  // equal keys: the lower expert stays
+#pragma unroll
+      for (int i = 0; i + w < kPer; i += 2 * w) {
+        const bool up = k[i + w] > k[i];
+        k[i] = up ? k[i + w] : k[i];
+        at[i] = up ? at[i + w] : at[i];
       }
+    const uint32_t top = __reduce_max_sync(0xffffffffu, k[0]);
+    const int e = __reduce_min_sync(0xffffffffu, k[0] == top ? at[0] : 0x7fffffff);
 #pragma unroll
-      for (int w = 1; w < kPer; w *= 2)  // equal keys: the lower expert stays
+    for (int i = 0; i < kPer; ++i) key[i] = lane + 32 * i == e ? 0u : key[i];
+    if (j == 0) first = top;
+    my_key = lane == j ? top : my_key;
+    my_e = lane == j ? e : my_e;
+  }
+  const float lmax = key_logit(first);
+  const float mine = lane < a.topk ? logit_exp(key_logit(my_key), lmax) : 0.0f;
+  float sum = mine;
+  if (!a.renorm) {
+    sum = 0.0f;
 #pragma unroll
-        for (int i = 0; i + w < kPer; i += 2 * w) {
-          const bool up = k[i + w] > k[i];
-          k[i] = up ? k[i + w] : k[i];
-          at[i] = up ? at[i + w] : at[i];
-        }
-      top = __reduce_max_sync(0xffffffffu, k[0]);
-      const int e = __reduce_min_sync(0xffffffffu, k[0] == top ? at[0] : 0x7fffffff);
+    for (int i = 0; i < kPer; ++i) sum += logit_exp(l[i], lmax);
+  }
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) key[i] = lane + 32 * i == e ? 0u : key[i];
-      if (j == 0) first = top;
-      my_key = lane == j ? top : my_key;
-      my_e = lane == j ? e : my_e;
-    }
-    const float lmax = key_logit(first);
-    const float mine = lane < a.topk ? logit_exp(key_logit(my_key), lmax) : 0.0f;
-    float sum = mine;
-    if (!a.renorm) {
-      sum = 0.0f;
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) sum += logit_exp(cur[i], lmax);
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (lane < a.topk) {
-      const int pr = t * a.topk + lane;
-      const float p = sum > 0.0f ? __fdiv_rn(mine, sum) : 0.0f;  // no logit above -inf: no expert counts
-      r.p[pr] = p;
-      sc.expert_of[pr] = p > 0.0f ? (short)my_e : (short)-1;  // weight 0: the expert is not evaluated
-      if (p > 0.0f) atomicOr(&sc.chose[2 * my_e + (t >> 5)], 1u << (t & 31));
-      if (publish) {
-        if (a.ids) a.ids[pr] = my_e;
-        if (a.weights) a.weights[pr] = p;
-      }
-    }
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  my_p = sum > 0.0f ? __fdiv_rn(mine, sum) : 0.0f;  // no logit above -inf: no expert counts
+}
+__device__ __forceinline__ void choose_any(const MoeArgs& a, int t, int& e, float& p) {
+  if (a.E <= 128)
+    choose<4>(a, t, e, p);
+  else
+    choose<kMoeMaxExperts / 32>(a, t, e, p);
+}
+__device__ __forceinline__ void publish_choice(const MoeArgs& a, int pr, int e, float p) {
+  if (a.ids) a.ids[pr] = e;
+  if (a.weights) a.weights[pr] = p;
+}
+
+// The choices of every token, a warp each, where they do not fit the first wave of
+// gate-up's own warps.
+constexpr int kChooseWarps = 8;
+__global__ void __launch_bounds__(32 * kChooseWarps) moe_choose_kernel(const MoeArgs a) {
+  pdl_trigger();
+  pdl_wait();
+  const int t = (int)(blockIdx.x * kChooseWarps + (threadIdx.x >> 5)), lane = threadIdx.x & 31;
+  if (t >= a.T) return;
+  int e;
+  float p;
+  choose_any(a, t, e, p);
+  if (lane < a.topk) {
+    const int pr = t * a.topk + lane;
+    a.choice_p[pr] = p;
+    a.choice[pr] = e;
+    publish_choice(a, pr, e, p);
   }
 }
 
@@ -180,15 +193,48 @@ __device__ __forceinline__ unsigned long long tokens_of(const RoutingScratch& sc
   return *reinterpret_cast<const unsigned long long*>(&sc.chose[2 * e]);
 }
 
-// The whole routing from the logits.  Ends with a barrier.
-template <int G>
+// The whole routing, from the logits (kChoose: at most a token per warp) or from
+// the choice kernel's list.  Every CTA derives the same.  Ends with a barrier.
+template <int G, bool kChoose>
 __device__ void build_routing(const MoeArgs& a, Routing& r, RoutingScratch& sc, bool publish) {
+  const int pairs = a.T * a.topk;
+  constexpr int kList = (kMaxPairs + kMoeThreads - 1) / kMoeThreads;
+  int le[kList];
+  float lp[kList];
+  if (!kChoose) {
+#pragma unroll
+    for (int j = 0; j < kList; ++j) {
+      const int i = j * kMoeThreads + (int)threadIdx.x;
+      le[j] = i < pairs ? __ldcg(a.choice + i) : 0;
+      lp[j] = i < pairs ? __ldcg(a.choice_p + i) : 0.0f;
+    }
+  }
   for (int i = threadIdx.x; i < 2 * a.E; i += kMoeThreads) sc.chose[i] = 0u;
   __syncthreads();
-  if (a.E <= 128)
-    choose_experts<4>(a, r, sc, publish);
-  else
-    choose_experts<kMoeMaxExperts / 32>(a, r, sc, publish);
+  auto enter = [&](int pr, int t, int e, float p) {
+    r.p[pr] = p;
+    sc.expert_of[pr] = p > 0.0f ? (short)e : (short)-1;  // weight 0: the expert is not evaluated
+    if (p > 0.0f) atomicOr(&sc.chose[2 * e + (t >> 5)], 1u << (t & 31));
+  };
+  if (kChoose) {
+    static_assert(!kChoose || kSmallGroup <= kMoeWarps, "a token per warp");
+    const int t = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (t < a.T) {
+      int e;
+      float p;
+      choose_any(a, t, e, p);
+      if (lane < a.topk) {
+        enter(t * a.topk + lane, t, e, p);
+        if (publish) publish_choice(a, t * a.topk + lane, e, p);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < kList; ++j) {
+      const int i = j * kMoeThreads + (int)threadIdx.x;
+      if (i < pairs) enter(i, i / a.topk, le[j], lp[j]);
+    }
+  }
   __syncthreads();
   if (threadIdx.x < 32) {  // lay the experts' pairs out one after another, in groups; a run of experts per lane
     const int per = (a.E + 31) / 32, e0 = threadIdx.x * per, e1 = min(a.E, e0 + per);
@@ -229,34 +275,6 @@ __device__ void build_routing(const MoeArgs& a, Routing& r, RoutingScratch& sc, 
     }
   }
   __syncthreads();
-}
-
-// The used parts of a routing to or from global memory, all threads.  Where the
-// parts end is known from the call alone, so every load is on its way at once.
-template <bool kRead>
-__device__ __forceinline__ void copy_routing(const MoeArgs& a, Routing& r, int* g) {
-  int* s = reinterpret_cast<int*>(&r);
-  const int pairs = a.T * a.topk, groups = min(pairs, kMaxGroups);
-  auto part = [&](size_t at, int n) {
-    const int w0 = (int)(at / 4);
-    for (int i0 = 0; i0 < n; i0 += 4 * kMoeThreads) {
-      int v[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int i = i0 + j * kMoeThreads + (int)threadIdx.x;
-        if (i < n) v[j] = kRead ? __ldcg(g + w0 + i) : s[w0 + i];
-      }
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int i = i0 + j * kMoeThreads + (int)threadIdx.x;
-        if (i < n) (kRead ? s : g)[w0 + i] = v[j];
-      }
-    }
-  };
-  part(0, 2 + pairs);                                                    // counts and p
-  part(offsetof(Routing, pairs), (pairs + 1) / 2);
-  part(offsetof(Routing, token), (pairs + 1) / 2);
-  part(offsetof(Routing, groups), groups * (int)(sizeof(Group) / 4));
 }
 
 // ------------------------------------------------------ columns on the fly ---
@@ -436,7 +454,7 @@ struct Up : MoeRing<kUpTerms, G, G == kSmallGroup ? 5 : 8> {
   static constexpr int kSmemBytes = Up::kBytes + 1024;
 };
 
-template <int G>
+template <int G, bool kChoose>
 __global__ void __launch_bounds__(kMoeThreads, G == kSmallGroup ? 2 : 1)
     moe_gate_up_kernel(const __grid_constant__ CUtensorMap map, const MoeArgs a) {
   using C = Up<G>;
@@ -450,9 +468,8 @@ __global__ void __launch_bounds__(kMoeThreads, G == kSmallGroup ? 2 : 1)
   moe_setup<C>(bars, &map);
   const uint32_t tmem = bars.tmem;
   pdl_wait();
-  build_routing<G>(a, r, *reinterpret_cast<RoutingScratch*>(smem), blockIdx.x == 0);
-  if (blockIdx.x == 0 && a.route) copy_routing<false>(a, r, a.route);
-  pdl_trigger();  // after the allocation, and after the logits of the kernels before are complete
+  build_routing<G, kChoose>(a, r, *reinterpret_cast<RoutingScratch*>(smem), blockIdx.x == 0);
+  pdl_trigger();  // after the allocation, and after the kernels before (logits, choices) are complete
   const int nkb = blocks_of(a.H), tiles = (a.I + kUpCols - 1) / kUpCols, items = r.n_groups * tiles;
   const int S = a.splits, rank = S > 1 ? (int)cluster_ctarank() : 0;
   const int cl = (int)blockIdx.x / S, ncl = (int)gridDim.x / S;  // with S > 1 there are as many clusters as items
@@ -596,22 +613,20 @@ __global__ void __launch_bounds__(kMoeThreads, G == kSmallGroup ? 2 : 1)
 // ------------------------------------------------------------------- down ---
 
 constexpr int kDownTerms = 3;
-// kEarly, for calls whose CTAs fit an SM beside gate-up's: derive the routing and
-// fill the ring with weights before gate-up has ended.  Otherwise gate-up's routing
-// is read once it has.
-template <int G, bool kEarly>
-struct Down : MoeRing<kDownTerms, G, kEarly ? 4 : (G == kSmallGroup ? 3 : 5)> {
+// kBeside: the form that fits an SM beside gate-up's (calls of up to 8 tokens).
+template <int G, bool kBeside>
+struct Down : MoeRing<kDownTerms, G, kBeside ? 4 : (G == kSmallGroup ? 3 : 5)> {
   static constexpr int kSums = Down::kBytes;  // [T][128]
   static constexpr int bytes(int T) { return kSums + T * kUnitRows * 4 + 1024; }
 };
-using EarlyDown = Down<kSmallGroup, true>;
-static_assert(Up<kSmallGroup>::kSmemBytes + EarlyDown::bytes(kSmallGroup) + 2 * (int)sizeof(Routing) <= 226 * 1024 &&
-              Up<kSmallGroup>::kTmem + EarlyDown::kTmem <= 512, "both kernels' forms share an SM");
+using BesideDown = Down<kSmallGroup, true>;
+static_assert(Up<kSmallGroup>::kSmemBytes + BesideDown::bytes(kSmallGroup) + 2 * (int)sizeof(Routing) <= 226 * 1024 &&
+              Up<kSmallGroup>::kTmem + BesideDown::kTmem <= 512, "both kernels' forms share an SM");
 
-template <int G, bool kEarly>
+template <int G, bool kBeside>
 __global__ void __launch_bounds__(kMoeThreads, G == kSmallGroup ? 2 : 1)
     moe_down_kernel(const __grid_constant__ CUtensorMap map, const MoeArgs a) {
-  using C = Down<G, kEarly>;
+  using C = Down<G, kBeside>;
   using Pos = RingPos<C::kStages>;
   extern __shared__ uint8_t smem_raw[];
   __shared__ Routing r;
@@ -620,22 +635,19 @@ __global__ void __launch_bounds__(kMoeThreads, G == kSmallGroup ? 2 : 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int S = a.splits, rank = S > 1 ? (int)cluster_ctarank() : 0;
-  const int d0 = (int)(blockIdx.x / S) * kUnitRows;
+  const int cl = (int)blockIdx.x / S, tile = cl / a.parts, part = cl - tile * a.parts;
+  const int d0 = tile * kUnitRows;
   const int nkb = blocks_of(a.I), rb = blocks_of(a.H);
   float* sums = reinterpret_cast<float*>(smem + C::kSums);
   moe_setup<C>(bars, &map);
   const uint32_t tmem = bars.tmem;
   pdl_trigger();  // after the allocation
-  if (kEarly) {  // logits and weights were complete before gate-up let this grid start
-    build_routing<G>(a, r, *reinterpret_cast<RoutingScratch*>(smem), false);
-  } else {
-    pdl_wait();
-    copy_routing<true>(a, r, a.route);
-    __syncthreads();
-  }
+  // Logits, choices and weights: complete before gate-up let this grid start.
+  build_routing<G, kBeside>(a, r, *reinterpret_cast<RoutingScratch*>(smem), false);
   for (int i = threadIdx.x; i < a.T * kUnitRows; i += kMoeThreads) sums[i] = 0.0f;
   const int units = r.n_groups * nkb;
-  const int u0 = (int)((long long)rank * units / S), u1 = (int)((long long)(rank + 1) * units / S);
+  const int share = part * S + rank, shares = a.parts * S;
+  const int u0 = (int)((long long)share * units / shares), u1 = (int)((long long)(share + 1) * units / shares);
   const uint64_t deadline = globaltimer_ns() + 2 * kWaitNs;  // gate-up may still run
   fence_proxy_async_smem();  // the scratch was written where copies land
   __syncthreads();
@@ -749,68 +761,110 @@ __global__ void __launch_bounds__(kMoeThreads, G == kSmallGroup ? 2 : 1)
     __syncthreads();
   // this CTA's share of the outputs, two neighbouring rows a thread
   const int pairs_of = a.T * (kUnitRows / 2);
+  const int i0 = rank * pairs_of / S, i1 = (rank + 1) * pairs_of / S;
   const uint32_t base = smem_u32(sums);
-  for (int i = rank * pairs_of / S + (int)threadIdx.x; i < (rank + 1) * pairs_of / S; i += kMoeThreads) {
+  float2* mine = reinterpret_cast<float2*>(a.partial) + (size_t)(tile * a.parts) * pairs_of;
+  auto store = [&](int i, float2 v) {
     const int t = i / (kUnitRows / 2), d = d0 + 2 * (i - t * (kUnitRows / 2));
-    if (d >= a.H || bars.abort) continue;
+    if (d >= a.H || bars.abort) return;
+    __nv_bfloat16* y = a.y + (size_t)t * a.ldy + d;
+    y[0] = __float2bfloat16_rn(v.x);
+    y[1] = __float2bfloat16_rn(v.y);
+  };
+  for (int i = i0 + (int)threadIdx.x; i < i1; i += kMoeThreads) {
     float2 v = make_float2(0.0f, 0.0f);
     for (int c = 0; c < S; ++c) {
       const float2 o = ld_shared_cluster_f2(S > 1 ? mapa_shared(base + i * 8, (uint32_t)c) : base + i * 8);
       v.x += o.x;
       v.y += o.y;
     }
-    __nv_bfloat16* y = a.y + (size_t)t * a.ldy + d;
-    y[0] = __float2bfloat16_rn(v.x);
-    y[1] = __float2bfloat16_rn(v.y);
+    if (a.parts == 1)
+      store(i, v);
+    else
+      __stcg(mine + (size_t)part * pairs_of + i, v);
+  }
+  if (a.parts > 1) {
+    // The last of the tile's CTAs of this rank adds the parts, in their order.
+    __shared__ int last;
+    __threadfence();
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      int* arrived = a.arrived + tile * 8 + rank;
+      last = atomicAdd(arrived, 1) == a.parts - 1;
+      if (last) *arrived = 0;
+    }
+    __syncthreads();
+    if (last) {
+      __threadfence();
+      for (int i = i0 + (int)threadIdx.x; i < i1; i += kMoeThreads) {
+        float2 v = make_float2(0.0f, 0.0f);
+        for (int q = 0; q < a.parts; ++q) {
+          const float2 o = __ldcg(mine + (size_t)q * pairs_of + i);
+          v.x += o.x;
+          v.y += o.y;
+        }
+        store(i, v);
+      }
+    }
   }
   if (S > 1) cluster_sync_all();  // no CTA leaves while a peer reads its sums
   moe_teardown<C>(tmem);
 }
 
-constexpr int kMaxCluster = 16;
-constexpr size_t kErrBytes = 256, kRouteBytes = (sizeof(Routing) + 255) / 256 * 256;
+constexpr int kMaxParts = 4, kMaxSharedTiles = 64;
+// The workspace: error word and arrivals at fixed places (they keep their meaning between calls of other sizes), then
+// the choices, h and the partial sums.
+constexpr size_t kFixedBytes = 256 + kMaxSharedTiles * 8 * sizeof(int);
+size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 
-template <int G, bool kEarly>
+template <int G, bool kFew>
 cudaError_t launch_form(MoeArgs& a, const uint8_t* w13, const uint8_t* w2, const Device* dev, cudaStream_t stream) {
   using U = Up<G>;
-  using D = Down<G, kEarly>;
+  using D = Down<G, kFew>;
   CUtensorMap m13, m2;
   if (!halves_map(&m13, w13, (uint64_t)a.E, (uint64_t)a.I, (uint64_t)a.H, 16) ||
       !byte_map(&m2, w2, (uint64_t)a.E * a.H, (uint64_t)a.I, kUnitRows))
     return cudaErrorInvalidValue;
   static bool up_done[64] = {}, down_done[64] = {};
-  const void *up = (const void*)moe_gate_up_kernel<G>, *down = (const void*)moe_down_kernel<G, kEarly>;
+  const void *up = (const void*)moe_gate_up_kernel<G, kFew>, *down = (const void*)moe_down_kernel<G, kFew>;
   cudaError_t e = opt_in_smem(up, U::kSmemBytes, up_done);
-  if (e == cudaSuccess) e = opt_in_smem(down, D::bytes(kEarly ? G : kMoeMaxTokens), down_done);
+  if (e == cudaSuccess) e = opt_in_smem(down, D::bytes(kFew ? G : kMoeMaxTokens), down_done);
   if (e != cudaSuccess) return e;
-  static bool wide_done[64] = {};
-  if ((e = allow_wide_clusters(down, wide_done)) != cudaSuccess) return e;
-  if (kEarly) a.route = nullptr;
+  if (!kFew) {
+    void* args[] = {&a};
+    e = launch_pdl((const void*)moe_choose_kernel, dim3((a.T + kChooseWarps - 1) / kChooseWarps),
+                   dim3(32 * kChooseWarps), 0, 1, stream, args);
+    if (e != cudaSuccess) return e;
+  }
   // Items if every choice were another expert; with few, clusters share them.
   // Otherwise as many CTAs as reside at once.
   const int pairs = a.T * a.topk, tiles = (a.I + kUpCols - 1) / kUpCols;
   const long long most = (long long)(pairs < a.E + pairs / G ? pairs : a.E + pairs / G) * tiles;
-  const int nkb = blocks_of(a.H);
+  const int nkb = blocks_of(a.H), resident = dev->sms * (G == kSmallGroup ? 2 : 1);
   a.splits = 1;
   while (a.splits < 8 && 2 * a.splits <= nkb && 2 * a.splits * most <= dev->sms) a.splits *= 2;
-  const int resident = dev->sms * (G == kSmallGroup ? 2 : 1);
   void* up_args[] = {&m13, &a};
-  e = launch_pdl(up, dim3((unsigned)((most < resident ? most : resident) * a.splits)),
-                 dim3(kMoeThreads), U::kSmemBytes, a.splits, stream, up_args);
+  e = launch_pdl(up, dim3((unsigned)((most < resident ? most : resident) * a.splits)), dim3(kMoeThreads),
+                 U::kSmemBytes, a.splits, stream, up_args);
   if (e != cudaSuccess) return e;
-  // the widest cluster with which every CTA resides at once
-  const int row_tiles = (a.H + kUnitRows - 1) / kUnitRows;
-  a.splits = kMaxCluster;
-  while (a.splits > 1 && row_tiles * a.splits > (kEarly ? dev->sms : resident)) a.splits /= 2;
+  // The widest cluster with which every CTA resides at once, and several to a tile where there are few tiles.
+  // (Clusters of 16 in place of two of 8 do not all find room on the GPU: measured 45 us more, a second wave.)
+  const int row_tiles = (a.H + kUnitRows - 1) / kUnitRows, room = kFew ? dev->sms : resident;
+  a.splits = 8;
+  while (a.splits > 1 && row_tiles * a.splits > room) a.splits /= 2;
+  a.parts = row_tiles <= kMaxSharedTiles ? room / (row_tiles * a.splits) : 1;
+  a.parts = a.parts < 1 ? 1 : (a.parts > kMaxParts ? kMaxParts : a.parts);
   void* down_args[] = {&m2, &a};
-  return launch_pdl(down, dim3((unsigned)(row_tiles * a.splits)), dim3(kMoeThreads),
-                    D::bytes(a.T), a.splits, stream, down_args);
+  return launch_pdl(down, dim3((unsigned)(row_tiles * a.splits * a.parts)), dim3(kMoeThreads), D::bytes(a.T), a.splits,
+                    stream, down_args);
 }
 
 }  // namespace
 
-size_t moe_workspace(int T, int topk, int I) {
-  return kErrBytes + kRouteBytes + (size_t)T * topk * I * sizeof(float);
+size_t moe_workspace(int T, int topk, int H, int I) {
+  const size_t pairs = (size_t)T * topk, tiles = (size_t)(H + kUnitRows - 1) / kUnitRows;
+  return kFixedBytes + align256(8 * pairs) + align256(pairs * I * sizeof(float)) +
+         (tiles <= kMaxSharedTiles ? kMaxParts * tiles * T * kUnitRows * sizeof(float) : 0);
 }
 
 cudaError_t launch_moe(const void* x, long long ldx, const float* logits, long long ldl, int T, int E, int topk,
@@ -829,8 +883,14 @@ cudaError_t launch_moe(const void* x, long long ldx, const float* logits, long l
   a.ids = ids;
   a.weights = weights;
   a.err = static_cast<int*>(ws);
-  a.route = reinterpret_cast<int*>(static_cast<uint8_t*>(ws) + kErrBytes);
-  a.h = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kErrBytes + kRouteBytes);
+  uint8_t* at = static_cast<uint8_t*>(ws);
+  const size_t pairs = (size_t)T * topk;
+  a.arrived = reinterpret_cast<int*>(at + 256);
+  a.choice = reinterpret_cast<int*>(at += kFixedBytes);
+  a.choice_p = reinterpret_cast<float*>(a.choice + pairs);
+  a.h = reinterpret_cast<float*>(at += align256(8 * pairs));
+  a.partial = reinterpret_cast<float*>(at += align256(pairs * I * sizeof(float)));
+  a.parts = 1;
   a.ldx = ldx;
   a.ldl = ldl;
   a.ldy = ldy;
