@@ -197,6 +197,27 @@ __device__ __forceinline__ unsigned long long tokens_of(const RoutingScratch& sc
 // the choice kernel's list.  Every CTA derives the same.  Ends with a barrier.
 template <int G, bool kChoose>
 __device__ void build_routing(const MoeArgs& a, Routing& r, RoutingScratch& sc, bool publish) {
+  if (kChoose && a.T == 1) {  // every choice is a group of its own, in the order of choice
+    if (threadIdx.x < 32) {
+      const int lane = threadIdx.x;
+      int e;
+      float p;
+      choose_any(a, 0, e, p);
+      const bool in = lane < a.topk && p > 0.0f;
+      const uint32_t all = __ballot_sync(0xffffffffu, in);
+      const int at = __popc(all & ((1u << lane) - 1u));
+      if (in) {
+        r.groups[at] = Group{(short)e, (short)at, 1, (short)tokens_form(1)};
+        r.pairs[at] = (short)lane;
+        r.token[at] = 0;
+        r.p[lane] = p;
+      }
+      if (lane == 0) r.n_groups = r.n_pairs = __popc(all);
+      if (publish && lane < a.topk) publish_choice(a, lane, e, p);
+    }
+    __syncthreads();
+    return;
+  }
   const int pairs = a.T * a.topk;
   constexpr int kList = (kMaxPairs + kMoeThreads - 1) / kMoeThreads;
   int le[kList];
@@ -415,6 +436,12 @@ struct MoeRing {
   static_assert(kTmem <= 512 && kStageBytes % 1024 == 0, "ring");
 };
 
+// Where part i of n begins among `total`.  In 32 bits: at most 544 groups of 2048
+// column tiles or 1024 k blocks, and a few hundred CTAs.
+__device__ __forceinline__ int share_of(int i, int total, int n) {
+  return (int)((uint32_t)i * (uint32_t)total / (uint32_t)n);
+}
+
 template <int P>
 struct Tokens {
   static constexpr int value = P;
@@ -473,7 +500,7 @@ __global__ void __launch_bounds__(kMoeThreads, G == kSmallGroup ? 2 : 1)
   const int nkb = blocks_of(a.H), tiles = (a.I + kUpCols - 1) / kUpCols, items = r.n_groups * tiles;
   const int S = a.splits, rank = S > 1 ? (int)cluster_ctarank() : 0;
   const int cl = (int)blockIdx.x / S, ncl = (int)gridDim.x / S;  // with S > 1 there are as many clusters as items
-  const int it0 = (int)((long long)cl * items / ncl), it1 = (int)((long long)(cl + 1) * items / ncl);
+  const int it0 = share_of(cl, items, ncl), it1 = share_of(cl + 1, items, ncl);
   const int b0 = rank * nkb / S, b1 = (rank + 1) * nkb / S;
   const uint64_t deadline = globaltimer_ns() + kWaitNs;
   fence_proxy_async_smem();  // the scratch was written where copies land
@@ -647,7 +674,7 @@ __global__ void __launch_bounds__(kMoeThreads, G == kSmallGroup ? 2 : 1)
   for (int i = threadIdx.x; i < a.T * kUnitRows; i += kMoeThreads) sums[i] = 0.0f;
   const int units = r.n_groups * nkb;
   const int share = part * S + rank, shares = a.parts * S;
-  const int u0 = (int)((long long)share * units / shares), u1 = (int)((long long)(share + 1) * units / shares);
+  const int u0 = share_of(share, units, shares), u1 = share_of(share + 1, units, shares);
   const uint64_t deadline = globaltimer_ns() + 2 * kWaitNs;  // gate-up may still run
   fence_proxy_async_smem();  // the scratch was written where copies land
   __syncthreads();
@@ -847,10 +874,11 @@ cudaError_t launch_form(MoeArgs& a, const uint8_t* w13, const uint8_t* w2, const
   e = launch_pdl(up, dim3((unsigned)((most < resident ? most : resident) * a.splits)), dim3(kMoeThreads),
                  U::kSmemBytes, a.splits, stream, up_args);
   if (e != cudaSuccess) return e;
-  // The widest cluster with which every CTA resides at once, and several to a tile where there are few tiles.
-  // (Clusters of 16 in place of two of 8 do not all find room on the GPU: measured 45 us more, a second wave.)
+  // The widest cluster with which every CTA resides at once, and several to a tile where there are few tiles.  With
+  // two CTAs on an SM clusters of 4: those of 8 (and 16) do not all find room in the GPU's SM groups, and one cluster
+  // that has to wait costs a second wave (45 us at 64 tokens).
   const int row_tiles = (a.H + kUnitRows - 1) / kUnitRows, room = kFew ? dev->sms : resident;
-  a.splits = 8;
+  a.splits = kFew ? 8 : 4;
   while (a.splits > 1 && row_tiles * a.splits > room) a.splits /= 2;
   a.parts = row_tiles <= kMaxSharedTiles ? room / (row_tiles * a.splits) : 1;
   a.parts = a.parts < 1 ? 1 : (a.parts > kMaxParts ? kMaxParts : a.parts);
