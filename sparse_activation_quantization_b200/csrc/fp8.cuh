@@ -133,13 +133,13 @@ __device__ __forceinline__ void tma_2d_pair(void* dst, const CUtensorMap* map, i
       "l"(map), "r"(bar_cluster), "r"(c0), "r"(c1)
       : "memory");
 }
-// 4-D tile -> shared memory
-__device__ __forceinline__ void tma_4d(void* dst, const CUtensorMap* map, int c0, int c1, int c2, int c3,
+// 5-D tile -> shared memory
+__device__ __forceinline__ void tma_5d(void* dst, const CUtensorMap* map, int c0, int c1, int c2, int c3, int c4,
                                        uint64_t* bar) {
   asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], "
+      "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6, %7}], "
       "[%2];" ::"r"(smem_u32(dst)),
-      "l"(map), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+      "l"(map), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4)
       : "memory");
 }
 __device__ __forceinline__ void tma_prefetch_map(const CUtensorMap* map) {
@@ -220,7 +220,8 @@ cudaError_t launch_pdl(const void* kernel, dim3 grid, dim3 block, int smem, int 
 // tensor map of a row-major byte matrix [rows][cols] with 128-byte swizzle and
 // a box of 128 columns x `box_rows` rows
 bool byte_map(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols, uint32_t box_rows);
-// the same of [E][halves][rows][cols], a box of 128 columns x `box_rows` rows x both halves
+// the same of [E][2][rows][cols], rows a multiple of 16, as {cols, 16, 2, rows / 16, E}: a box of 128 columns and
+// `box_rows` rows of both halves, 16 of one and 16 of the other in turn
 bool halves_map(CUtensorMap* map, const void* base, uint64_t E, uint64_t rows, uint64_t cols, uint32_t box_rows);
 
 }  // namespace fp8

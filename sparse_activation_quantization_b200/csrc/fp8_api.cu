@@ -85,7 +85,7 @@ bool tensor_map(CUtensorMap* map, const void* base, int rank, const cuuint64_t* 
       return false;
     encode = reinterpret_cast<Encode>(f);
   }
-  const cuuint32_t elem[4] = {1, 1, 1, 1};
+  const cuuint32_t elem[5] = {1, 1, 1, 1, 1};
   return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, (cuuint32_t)rank, const_cast<void*>(base), dims, strides, box, elem,
                 CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
@@ -99,9 +99,10 @@ bool byte_map(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols, 
 }
 
 bool halves_map(CUtensorMap* map, const void* base, uint64_t E, uint64_t rows, uint64_t cols, uint32_t box_rows) {
-  const cuuint64_t dims[4] = {cols, rows, 2, E}, strides[3] = {cols, rows * cols, 2 * rows * cols};
-  const cuuint32_t box[4] = {128, box_rows, 2, 1};
-  return tensor_map(map, base, 4, dims, strides, box);
+  const cuuint64_t dims[5] = {cols, 16, 2, rows / 16, E};
+  const cuuint64_t strides[4] = {cols, rows * cols, 16 * cols, 2 * rows * cols};
+  const cuuint32_t box[5] = {128, 16, 2, box_rows / 16, 1};
+  return tensor_map(map, base, 5, dims, strides, box);
 }
 
 }  // namespace fp8

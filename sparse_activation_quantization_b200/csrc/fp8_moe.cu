@@ -327,10 +327,13 @@ struct Raw8 {
 // Block b of np tokens into a stage's B operand (128-byte swizzle) and scales, by
 // one warp: half a warp per token, eight values a lane, kBatch tokens of each half
 // side by side.  rows(n): token n's row; weights(n): a factor of its scale.
-// Columns of no token keep what they held: their sums are not used.
-template <int J, class T, int kBatch, class Rows, class Weights>
+// Columns of no token keep what they held: their sums are not used.  ready():
+// returns once the stage is free.  It is asked only when the first terms are at
+// hand, so that loads and arithmetic lie outside the ring's round trip (they are
+// 2000 of its 3300 cycles at one token).
+template <int J, class T, int kBatch, class Rows, class Weights, class Ready>
 __device__ __forceinline__ void form_batch(uint8_t* dst, float* scale, int n0, int np, int P, int b, int K, Rows rows,
-                                           Weights weights) {
+                                           Weights weights, Ready ready) {
   const int lane = threadIdx.x & 31, l16 = lane & 15, half = lane >> 4;
   const int k = b * kBlock + l16 * 8;
   Raw8<T> raw[kBatch];  // every load is on its way before the first value is used
@@ -352,6 +355,7 @@ __device__ __forceinline__ void form_batch(uint8_t* dst, float* scale, int n0, i
   for (int o = 8; o > 0; o >>= 1)
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) m[i] = fmaxf(m[i], __shfl_xor_sync(0xffffffffu, m[i], o));
+  float sc[kBatch];
 #pragma unroll
   for (int i = 0; i < kBatch; ++i) {
     const int n = n0 + 2 * i + half;
@@ -360,19 +364,17 @@ __device__ __forceinline__ void form_batch(uint8_t* dst, float* scale, int n0, i
     const float up = __uint_as_float((261u - ef) << 23);
 #pragma unroll
     for (int e = 0; e < 8; ++e) f[i][e] *= up;
-    if (n < np && l16 == 0)  // an infinity saturates in E4M3: it is in the scale
-      scale[n] = (ef == 255u ? INFINITY : __uint_as_float((ef - 7u) << 23)) * weights(n);
+    // an infinity saturates in E4M3: it is in the scale
+    sc[i] = (ef == 255u ? INFINITY : __uint_as_float((ef - 7u) << 23)) * (n < np ? weights(n) : 1.0f);
   }
+  uint2 term[kBatch][J];
 #pragma unroll
   for (int j = 0; j < J; ++j)
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
-      const int n = n0 + 2 * i + half;
       float(&v)[8] = f[i];
       const uint32_t c0 = e4m3x4(v[0], v[1], v[2], v[3]), c1 = e4m3x4(v[4], v[5], v[6], v[7]);
-      if (n < np)
-        *reinterpret_cast<uint2*>(dst + codes_chunk_off((uint32_t)(j * P + n), l16 >> 1) + (l16 & 1) * 8) =
-            make_uint2(c0, c1);
+      term[i][j] = make_uint2(c0, c1);
       if (j + 1 < J) {
         const float2 d0 = e4m3x2_to_float(c0), d1 = e4m3x2_to_float(c0 >> 16);
         const float2 d2 = e4m3x2_to_float(c1), d3 = e4m3x2_to_float(c1 >> 16);
@@ -382,16 +384,34 @@ __device__ __forceinline__ void form_batch(uint8_t* dst, float* scale, int n0, i
         v[6] = (v[6] - d3.x) * 16.0f, v[7] = (v[7] - d3.y) * 16.0f;
       }
     }
+  if (!ready()) return;
+#pragma unroll
+  for (int i = 0; i < kBatch; ++i) {
+    const int n = n0 + 2 * i + half;
+    if (n < np) {
+      if (l16 == 0) scale[n] = sc[i];
+#pragma unroll
+      for (int j = 0; j < J; ++j)
+        *reinterpret_cast<uint2*>(dst + codes_chunk_off((uint32_t)(j * P + n), l16 >> 1) + (l16 & 1) * 8) = term[i][j];
+    }
+  }
 }
-template <int J, class T, class Rows, class Weights>
-__device__ __forceinline__ void form_columns(uint8_t* dst, float* scale, int np, int P, int b, int K, Rows rows,
-                                             Weights weights) {
+// Returns false if the stage did not become free.
+template <int J, class T, class Rows, class Weights, class Wait>
+__device__ __forceinline__ bool form_columns(uint8_t* dst, float* scale, int np, int P, int b, int K, Rows rows,
+                                             Weights weights, Wait wait) {
+  bool free = false;
+  auto ready = [&]() {
+    if (!free) free = __all_sync(0xffffffffu, wait());
+    return free;
+  };
   int n0 = 0;
-  for (; np - n0 > 4; n0 += 8) form_batch<J, T, 4>(dst, scale, n0, np, P, b, K, rows, weights);
+  for (; np - n0 > 4; n0 += 8) form_batch<J, T, 4>(dst, scale, n0, np, P, b, K, rows, weights, ready);
   if (np - n0 > 2)
-    form_batch<J, T, 2>(dst, scale, n0, np, P, b, K, rows, weights);
+    form_batch<J, T, 2>(dst, scale, n0, np, P, b, K, rows, weights, ready);
   else if (np > n0)
-    form_batch<J, T, 1>(dst, scale, n0, np, P, b, K, rows, weights);
+    form_batch<J, T, 1>(dst, scale, n0, np, P, b, K, rows, weights, ready);
+  return free;
 }
 
 __host__ __device__ constexpr int mma_n(int cols) { return (cols + 15) / 16 * 16; }
@@ -517,11 +537,8 @@ __global__ void __launch_bounds__(kMoeThreads, G == kSmallGroup ? 2 : 1)
             bars.give_up(a.err);
             break;
           }
-          uint8_t* st = smem + p.s * C::kStageBytes;
           mbar_arrive_expect_tx(&bars.full[p.s], kUnitBytes);
-#pragma unroll
-          for (int w = 0; w < kUpCols / 16; ++w)
-            tma_4d(st + w * 32 * kBlock, &map, b * kBlock, i0 + 16 * w, 0, e, &bars.full[p.s]);
+          tma_5d(smem + p.s * C::kStageBytes, &map, b * kBlock, 0, 0, i0 / 16, e, &bars.full[p.s]);
         }
       }
       if (bars.abort) drain_copies(bars, n);
@@ -551,13 +568,13 @@ __global__ void __launch_bounds__(kMoeThreads, G == kSmallGroup ? 2 : 1)
       for (int b = b0; b < b1; ++b, p.next()) {
         if (turn-- > 0) continue;
         turn = C::kFormers - 1;
-        if (!__all_sync(0xffffffffu, wait_empty(bars, p, deadline))) {
+        if (!form_columns<kUpTerms, __nv_bfloat16>(
+                smem + p.s * C::kStageBytes + kUnitBytes, scale[p.s], gr.count, gr.form, b, a.H,
+                [&](int n) { return a.x + (size_t)r.token[gr.first + n] * a.ldx; }, [](int) { return 1.0f; },
+                [&]() { return wait_empty(bars, p, deadline); })) {
           bars.give_up(a.err);
           break;
         }
-        form_columns<kUpTerms, __nv_bfloat16>(
-            smem + p.s * C::kStageBytes + kUnitBytes, scale[p.s], gr.count, gr.form, b, a.H,
-            [&](int n) { return a.x + (size_t)r.token[gr.first + n] * a.ldx; }, [](int) { return 1.0f; });
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive_cta(&bars.full[p.s]);
@@ -718,14 +735,13 @@ __global__ void __launch_bounds__(kMoeThreads, G == kSmallGroup ? 2 : 1)
       if ((u - u0) % C::kFormers != warp - kFirstFormWarp) continue;
       const int grp = u / nkb;
       const Group gr = r.groups[grp];
-      if (!__all_sync(0xffffffffu, wait_empty(bars, p, deadline))) {
+      if (!form_columns<kDownTerms, float>(
+              smem + p.s * C::kStageBytes + kUnitBytes, scale[p.s], gr.count, gr.form, u - grp * nkb, a.I,
+              [&](int n) { return a.h + (size_t)r.pairs[gr.first + n] * a.I; },
+              [&](int n) { return r.p[r.pairs[gr.first + n]]; }, [&]() { return wait_empty(bars, p, deadline); })) {
         bars.give_up(a.err);
         break;
       }
-      form_columns<kDownTerms, float>(
-          smem + p.s * C::kStageBytes + kUnitBytes, scale[p.s], gr.count, gr.form, u - grp * nkb, a.I,
-          [&](int n) { return a.h + (size_t)r.pairs[gr.first + n] * a.I; },
-          [&](int n) { return r.p[r.pairs[gr.first + n]]; });
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive_cta(&bars.full[p.s]);
@@ -799,12 +815,16 @@ __global__ void __launch_bounds__(kMoeThreads, G == kSmallGroup ? 2 : 1)
     y[1] = __float2bfloat16_rn(v.y);
   };
   for (int i = i0 + (int)threadIdx.x; i < i1; i += kMoeThreads) {
-    float2 v = make_float2(0.0f, 0.0f);
-    for (int c = 0; c < S; ++c) {
-      const float2 o = ld_shared_cluster_f2(S > 1 ? mapa_shared(base + i * 8, (uint32_t)c) : base + i * 8);
-      v.x += o.x;
-      v.y += o.y;
-    }
+    float2 o[8], v = make_float2(0.0f, 0.0f);  // every load is on its way before the first sum
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+      if (c < S) o[c] = ld_shared_cluster_f2(S > 1 ? mapa_shared(base + i * 8, (uint32_t)c) : base + i * 8);
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+      if (c < S) {
+        v.x += o[c].x;
+        v.y += o[c].y;
+      }
     if (a.parts == 1)
       store(i, v);
     else
@@ -849,7 +869,7 @@ cudaError_t launch_form(MoeArgs& a, const uint8_t* w13, const uint8_t* w2, const
   using U = Up<G>;
   using D = Down<G, kFew>;
   CUtensorMap m13, m2;
-  if (!halves_map(&m13, w13, (uint64_t)a.E, (uint64_t)a.I, (uint64_t)a.H, 16) ||
+  if (!halves_map(&m13, w13, (uint64_t)a.E, (uint64_t)a.I, (uint64_t)a.H, kUpCols) ||
       !byte_map(&m2, w2, (uint64_t)a.E * a.H, (uint64_t)a.I, kUnitRows))
     return cudaErrorInvalidValue;
   static bool up_done[64] = {}, down_done[64] = {};
