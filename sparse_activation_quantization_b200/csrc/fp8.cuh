@@ -83,6 +83,10 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
+__device__ __forceinline__ void prefetch_l1(const void* p) {
+  asm volatile("prefetch.global.L1 [%0];" ::"l"(p) : "memory");
+}
+
 __device__ __forceinline__ void record_error_word(int* err, int code) {
   if (err) atomicCAS(err, 0, code);
 }
@@ -142,6 +146,15 @@ __device__ __forceinline__ void tma_5d(void* dst, const CUtensorMap* map, int c0
       "l"(map), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4)
       : "memory");
 }
+// shared memory -> 2-D tile, of which only what lies inside the map is written;
+// part of this thread's bulk group
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, const void* src, int c0, int c1) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(map),
+               "r"(smem_u32(src)), "r"(c0), "r"(c1)
+               : "memory");
+}
+// every bulk store of this thread has been written
+__device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 __device__ __forceinline__ void tma_prefetch_map(const CUtensorMap* map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }
@@ -220,7 +233,10 @@ cudaError_t launch_pdl(const void* kernel, dim3 grid, dim3 block, int smem, int 
 // tensor map of a row-major byte matrix [rows][cols] with 128-byte swizzle and
 // a box of 128 columns x `box_rows` rows
 bool byte_map(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols, uint32_t box_rows);
-// the same of [E][2][rows][cols], rows a multiple of 16, as {cols, 16, 2, rows / 16, E}: a box of 128 columns and
+// tensor map of rows of `cols` elements of 2 (bf16) or 4 (float32) bytes, `ld` elements apart, with 128-byte swizzle and
+// a box of 128 bytes x `box_rows` rows; the base and the rows start on 16-byte boundaries
+bool rows_map(CUtensorMap* map, void* base, uint64_t rows, uint64_t cols, uint64_t ld, int bytes, uint32_t box_rows);
+// byte map of [E][2][rows][cols], rows a multiple of 16, as {cols, 16, 2, rows / 16, E}: a box of 128 columns and
 // `box_rows` rows of both halves, 16 of one and 16 of the other in turn
 bool halves_map(CUtensorMap* map, const void* base, uint64_t E, uint64_t rows, uint64_t cols, uint32_t box_rows);
 

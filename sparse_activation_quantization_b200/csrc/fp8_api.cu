@@ -69,9 +69,8 @@ cudaError_t launch_pdl(const void* kernel, dim3 grid, dim3 block, int smem, int 
 }
 
 namespace {
-// tensor map of bytes, 128-byte swizzle; dims, strides (of all but the first axis) and box innermost first
-bool tensor_map(CUtensorMap* map, const void* base, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
-                const cuuint32_t* box) {
+// tensor map with 128-byte swizzle; dims, strides (of all but the first axis) and box innermost first
+bool tensor_map(CUtensorMap* map, CUtensorMapDataType type, const void* base, int rank, const cuuint64_t* dims, const cuuint64_t* strides, const cuuint32_t* box) {
   using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                               const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                               CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
@@ -86,7 +85,7 @@ bool tensor_map(CUtensorMap* map, const void* base, int rank, const cuuint64_t* 
     encode = reinterpret_cast<Encode>(f);
   }
   const cuuint32_t elem[5] = {1, 1, 1, 1, 1};
-  return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, (cuuint32_t)rank, const_cast<void*>(base), dims, strides, box, elem,
+  return encode(map, type, (cuuint32_t)rank, const_cast<void*>(base), dims, strides, box, elem,
                 CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -95,14 +94,21 @@ bool tensor_map(CUtensorMap* map, const void* base, int rank, const cuuint64_t* 
 bool byte_map(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols, uint32_t box_rows) {
   const cuuint64_t dims[2] = {cols, rows}, strides[1] = {cols};
   const cuuint32_t box[2] = {128, box_rows};
-  return tensor_map(map, base, 2, dims, strides, box);
+  return tensor_map(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, base, 2, dims, strides, box);
+}
+
+bool rows_map(CUtensorMap* map, void* base, uint64_t rows, uint64_t cols, uint64_t ld, int bytes, uint32_t box_rows) {
+  const cuuint64_t dims[2] = {cols, rows}, strides[1] = {ld * bytes};
+  const cuuint32_t box[2] = {128u / (uint32_t)bytes, box_rows};
+  return tensor_map(map, bytes == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, 2, dims,
+                    strides, box);
 }
 
 bool halves_map(CUtensorMap* map, const void* base, uint64_t E, uint64_t rows, uint64_t cols, uint32_t box_rows) {
   const cuuint64_t dims[5] = {cols, 16, 2, rows / 16, E};
   const cuuint64_t strides[4] = {cols, rows * cols, 16 * cols, 2 * rows * cols};
   const cuuint32_t box[5] = {128, 16, 2, box_rows / 16, 1};
-  return tensor_map(map, base, 5, dims, strides, box);
+  return tensor_map(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, base, 5, dims, strides, box);
 }
 
 }  // namespace fp8

@@ -439,81 +439,100 @@ __global__ void __launch_bounds__(Tile::kThreads, 1)
 // Two CTAs of a cluster run each 256 x 256 output tile as one tensor-core unit
 // (M = 256): CTA r holds rows 128 r .. of X and columns 128 r .. of W, so each
 // operand byte crosses from L2 once per 256 rows or columns of the other.
-//   both CTAs  producer (warp 0): its own two boxes per 128-k block; their
-//              bytes count on the even CTA's barrier
-//              consumers (warps 4-11): its own 128 rows, a thread holds one row
-//              and 128 columns (one weight-scale block) in registers
-//   even CTA   MMA issuer (warp 1), two 256-column TMEM buffers; its commits
-//              arrive on both CTAs' barriers
-// The consumers take 224 registers (setmaxnreg), the other four warps keep 56:
+//   warps 4-11  sums of the CTA's own 128 rows: a thread holds one row and 128
+//               columns (one weight-scale block)
+//   warp 0      one thread copies: the CTA's own two boxes per 128-k block; their
+//               bytes count on the even CTA's barrier
+//   warp 1      TMEM allocation; in the even CTA one thread issues the MMAs into
+//               two 256-column TMEM buffers; its commits arrive on both CTAs'
+//               barriers
+// A block's four MMAs take about 520 cycles.  Adding its 256 columns takes each
+// warp scheduler 256 cycles of the FMA pipe, so everything else a sum warp does
+// per block has to hide behind that: a 32-column piece is read while the one
+// before is added, over the block's end as well, and the scales come ahead.
+// Waits acquire at CTA scope: what they guard is TMEM (ordered by the tcgen05
+// fences) and bytes of the copy engine.  (At cluster scope a wait that need not
+// wait takes 250 cycles.)
+// The sum warps take 224 registers (setmaxnreg), the other four keep 56:
 // 256 x 224 + 128 x 56 = 384 x 168, the launch's registers.
+// Output goes through 8 KB of shared memory per warp and leaves by a tensor-map
+// store, so the next tile's sums start at once.
 
 struct Pair {
   static constexpr int BM = 256, BN = 256;
-  static constexpr int kStages = 6;
+  static constexpr int kStages = 5;
   static constexpr int kStageBytes = 2 * 16384;
   static constexpr int kBufs = 2;
-  static constexpr int kThreads = 384;
-  static constexpr int kRegsLaunch = 168, kRegsConsumer = 224, kRegsOther = 56;
-  static constexpr int kOffStage = kStages * kStageBytes;  // 4 KB of output staging per consumer warp
-  static constexpr int kSmemBytes = kOffStage + 8 * 4096 + 1024;
+  static constexpr int kSums = 8;  // warps
+  static constexpr int kAhead = 5;  // blocks that scales of X are brought near before they are due
+  static constexpr int kThreads = 32 * (kSums + 4);
+  static constexpr int kRegsLaunch = 168, kRegsSum = 224, kRegsOther = 56;
+  static constexpr int kOffStage = kStages * kStageBytes;
+  static constexpr int kSmemBytes = kOffStage + kSums * 8192 + 1024;
   static_assert(kSmemBytes <= 232448 - 1024, "shared memory overflow");
-  static_assert(2 * kRegsConsumer + kRegsOther <= 3 * kRegsLaunch, "register split above the launch's share");
+  static_assert(2 * kRegsSum + kRegsOther <= 3 * kRegsLaunch, "register split above the launch's share");
 };
-__device__ __forceinline__ void regs_consumer() { asm volatile("setmaxnreg.inc.sync.aligned.u32 224;" ::: "memory"); }
+__device__ __forceinline__ void regs_sum() { asm volatile("setmaxnreg.inc.sync.aligned.u32 224;" ::: "memory"); }
 __device__ __forceinline__ void regs_other() { asm volatile("setmaxnreg.dec.sync.aligned.u32 56;" ::: "memory"); }
 
-// 32 rows (row = lane) x 32 four-byte words held in registers -> Y through the
-// warp's 4 KB of shared memory, so that a warp stores whole 128-byte lines.
-// kWords: output elements per word (2 for bf16, 1 for float32).
-template <int kPer>
-__device__ __forceinline__ void store_rows(const LinearArgs& a, uint8_t* wst, const uint32_t (&v)[32], int row0,
-                                           int rows, int col0, int lane) {
+// 32 rows (row = lane) x 128 bytes in registers -> the warp's staging area, with
+// the 128-byte swizzle of the output's tensor map
+__device__ __forceinline__ void stage_rows(uint8_t* wst, const uint32_t (&v)[32], int lane) {
 #pragma unroll
   for (int j = 0; j < 8; ++j)
-    *reinterpret_cast<uint4*>(wst + lane * 128 + ((j ^ (lane & 7)) << 4)) =
+    *reinterpret_cast<uint4*>(wst + codes_chunk_off((uint32_t)lane, (uint32_t)j)) =
         make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-  __syncwarp();
+}
+// The staged rows to rows of Y that no tensor map describes.  kPer: output
+// elements per four bytes (2 for bf16, 1 for float32).
+template <int kPer>
+__device__ __forceinline__ void copy_rows(const LinearArgs& a, const uint8_t* wst, int row0, int col0, int lane) {
   constexpr int kEl = 4 / kPer;  // bytes per element
   uint8_t* y = static_cast<uint8_t*>(a.y);
-  if (a.vec_y && col0 + 32 * kPer <= a.D) {
-    const int rsub = lane >> 3, q = lane & 7;
+  const int rows = min(32, a.T - row0);
+  for (int r = 0; r < rows; ++r) {
 #pragma unroll
-    for (int it = 0; it < 8; ++it) {
-      const int r = 4 * it + rsub;
-      if (r < rows)
-        *reinterpret_cast<uint4*>(y + ((size_t)(row0 + r) * a.ldy + col0) * kEl + 16 * q) =
-            *reinterpret_cast<const uint4*>(wst + r * 128 + ((q ^ (r & 7)) << 4));
-    }
-  } else {
-    for (int r = 0; r < rows && r < 32; ++r) {
-#pragma unroll
-      for (int e = 0; e < kPer; ++e) {
-        const int c = lane + 32 * e;  // element of the row's 32 * kPer
-        const int byte = c * kEl;
-        const uint8_t* src = wst + r * 128 + (((byte >> 4) ^ (r & 7)) << 4) + (byte & 15);
-        if (col0 + c < a.D) {
-          uint8_t* dst = y + ((size_t)(row0 + r) * a.ldy + col0 + c) * kEl;
-          if (kPer == 2)
-            *reinterpret_cast<uint16_t*>(dst) = *reinterpret_cast<const uint16_t*>(src);
-          else
-            *reinterpret_cast<uint32_t*>(dst) = *reinterpret_cast<const uint32_t*>(src);
-        }
+    for (int e = 0; e < kPer; ++e) {
+      const int c = lane + 32 * e, byte = c * kEl;  // element of the row's 32 * kPer
+      const uint8_t* src = wst + codes_chunk_off((uint32_t)r, (uint32_t)byte >> 4) + (byte & 15);
+      if (col0 + c < a.D) {
+        uint8_t* dst = y + ((size_t)(row0 + r) * a.ldy + col0 + c) * kEl;
+        if (kPer == 2)
+          *reinterpret_cast<uint16_t*>(dst) = *reinterpret_cast<const uint16_t*>(src);
+        else
+          *reinterpret_cast<uint32_t*>(dst) = *reinterpret_cast<const uint32_t*>(src);
       }
     }
   }
   __syncwarp();
 }
+// 32 rows x 32 four-byte words of output through 4 KB of staging, which no store reads any more
+template <int kPer>
+__device__ __forceinline__ void put_rows(const LinearArgs& a, const CUtensorMap* mapy, uint8_t* wst,
+                                         const uint32_t (&v)[32], int row0, int col0, int lane) {
+  stage_rows(wst, v, lane);
+  if (a.vec_y) {
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+      tma_store_2d(mapy, wst, col0, row0);
+      bulk_commit_group();
+    }
+  } else {
+    __syncwarp();
+    copy_rows<kPer>(a, wst, row0, col0, lane);
+  }
+}
 
 __global__ void __launch_bounds__(Pair::kThreads, 1)
     fp8_pair_kernel(const __grid_constant__ CUtensorMap mapx, const __grid_constant__ CUtensorMap mapw,
-                    const LinearArgs a) {
+                    const __grid_constant__ CUtensorMap mapy, const LinearArgs a) {
   using C = Pair;
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t full_bar[C::kStages];   // even CTA: both CTAs' boxes have landed
   __shared__ __align__(8) uint64_t empty_bar[C::kStages];  // each CTA: its slot has been read
   __shared__ __align__(8) uint64_t acc_full[C::kBufs];     // each CTA
-  __shared__ __align__(8) uint64_t acc_empty[C::kBufs];    // even CTA: both CTAs' consumers took the buffer
+  __shared__ __align__(8) uint64_t acc_empty[C::kBufs];    // even CTA: both CTAs' sum warps took the buffer
   __shared__ uint32_t tmem_base_sh;
   __shared__ volatile int abort_sh;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -546,7 +565,7 @@ __global__ void __launch_bounds__(Pair::kThreads, 1)
     }
     for (int b = 0; b < C::kBufs; ++b) {
       mbar_init(&acc_full[b], 1);
-      mbar_init(&acc_empty[b], 16);  // 8 consumer warps of each CTA
+      mbar_init(&acc_empty[b], 2 * C::kSums);
     }
     fence_mbar_init();
     abort_sh = 0;
@@ -567,14 +586,14 @@ __global__ void __launch_bounds__(Pair::kThreads, 1)
     regs_other();
     if (warp == 0 && elect_one()) {
       const uint32_t full_lead = mapa_shared(smem_u32(&full_bar[0]), 0);
-      int i = 0;
+      int i = 0, s = 0;
+      uint32_t phase = 1;  // of the slot's previous use
       for (int tile = pair; tile < ntiles && !abort_sh; tile += npairs) {
         int mt, nt;
         coords(tile, mt, nt);
         const uint64_t deadline = globaltimer_ns() + kWaitNs;
         for (int b = 0; b < nkb; ++b, ++i) {
-          const int s = i % C::kStages;
-          if (i >= C::kStages && !mbar_wait_cluster(&empty_bar[s], ((i / C::kStages) & 1) ^ 1, deadline, &abort_sh)) {
+          if (i >= C::kStages && !mbar_wait(&empty_bar[s], phase, deadline, &abort_sh)) {
             record_error_word(a.err, kErrTimeoutWord);
             abort_sh = 1;
             break;
@@ -584,6 +603,10 @@ __global__ void __launch_bounds__(Pair::kThreads, 1)
           const uint32_t fb = full_lead + (uint32_t)(s * sizeof(uint64_t));
           tma_2d_pair(st, &mapx, b * kBlock, mt * C::BM + (int)rank * 128, fb);
           tma_2d_pair(st + 16384, &mapw, b * kBlock, nt * C::BN + (int)rank * 128, fb);
+          if (++s == C::kStages) {
+            s = 0;
+            phase ^= 1;
+          }
         }
       }
       // every slot's last use has been released (so its copies landed and the
@@ -592,15 +615,17 @@ __global__ void __launch_bounds__(Pair::kThreads, 1)
       for (int j = i > C::kStages ? i - C::kStages : 0; j < i; ++j)
         while (!mbar_try_wait_cluster(&empty_bar[j % C::kStages], (j / C::kStages) & 1) && globaltimer_ns() < lim) {
         }
-    } else if (warp == 1 && leader && elect_one()) {
+    }
+    if (warp == 1 && leader && elect_one()) {
       constexpr uint32_t idesc = idesc_e4m3(C::BM, C::BN);
-      int i = 0;
+      int i = 0, s = 0;
+      uint32_t phase = 0;
       for (int tile = pair; tile < ntiles && !abort_sh; tile += npairs) {
         const uint64_t deadline = globaltimer_ns() + kWaitNs;
         for (int b = 0; b < nkb; ++b, ++i) {
-          const int s = i % C::kStages, u = i % C::kBufs;
-          if (!mbar_wait_cluster(&full_bar[s], (i / C::kStages) & 1, deadline, &abort_sh) ||
-              (i >= C::kBufs && !mbar_wait_cluster(&acc_empty[u], ((i / C::kBufs) & 1) ^ 1, deadline, &abort_sh))) {
+          const int u = i & 1;
+          if (!mbar_wait(&full_bar[s], phase, deadline, &abort_sh) ||
+              (i >= C::kBufs && !mbar_wait(&acc_empty[u], ((i >> 1) & 1) ^ 1, deadline, &abort_sh))) {
             record_error_word(a.err, kErrTimeoutWord);
             abort_sh = 1;
             break;
@@ -613,47 +638,69 @@ __global__ void __launch_bounds__(Pair::kThreads, 1)
                         smem_desc(st + 16384 + 32 * j, 16, 1024, kSw128), idesc, j > 0);
           tc_commit_pair_mc(&empty_bar[s], 0x3);
           tc_commit_pair_mc(&acc_full[u], 0x3);
+          if (++s == C::kStages) {
+            s = 0;
+            phase ^= 1;
+          }
         }
       }
     }
   } else {
-    regs_consumer();
-    const int sp = warp & 3, half = (warp - 4) >> 2;
+    regs_sum();
+    const int sp = warp & 3, half = (warp - 4) >> 2;  // TMEM lane quarter; column half
     const uint32_t acc_empty_lead = mapa_shared(smem_u32(&acc_empty[0]), 0);
-    uint8_t* wst = smem + C::kOffStage + (size_t)(warp - 4) * 4096;
+    uint8_t* wst = smem + C::kOffStage + (size_t)(warp - 4) * 8192;
     const int d_blocks = blocks_of(a.D);
+    const uint32_t src = tmem + ((uint32_t)(sp * 32) << 16) + half * 128;
+    uint64_t deadline = globaltimer_ns() + kWaitNs;
+    // Where a wait runs out the warp goes on as one, with sums that nobody stores.
+    auto wait_block = [&](int i) {
+      if (!mbar_wait(&acc_full[i & 1], (i >> 1) & 1, deadline, &abort_sh)) {
+        record_error_word(a.err, kErrTimeoutWord);
+        abort_sh = 1;
+      }
+      __syncwarp();
+      tc_fence_after();
+    };
     int i = 0;
+    uint32_t v[2][32];
+    if (pair < ntiles) {
+      wait_block(0);
+      tmem_ld32(src, v[0]);
+    }
     for (int tile = pair; tile < ntiles && !abort_sh; tile += npairs) {
       int mt, nt;
       coords(tile, mt, nt);
-      const uint64_t deadline = globaltimer_ns() + kWaitNs;
+      const bool more = tile + npairs < ntiles;
+      deadline = globaltimer_ns() + kWaitNs;
       const int row0 = mt * C::BM + (int)rank * 128 + sp * 32;
-      const int nb = nt * 2 + half;  // this thread's weight-scale block
       const float* xs = a.xs + min(row0 + lane, a.T - 1);
-      const float* ws = a.ws + (size_t)min(nb, d_blocks - 1) * nkb;
+      ScaleRow ws;
+      ws.start(a.ws + (size_t)min(nt * 2 + half, d_blocks - 1) * nkb, nkb, 0, lane);
       float acc[128] = {};
-      float s_next = xs[0] * ws[0];
+      float x_next = *xs;
+      for (int b = 1; b < C::kAhead && b < nkb; ++b) prefetch_l1(xs + (size_t)b * a.lds);
       for (int b = 0; b < nkb; ++b, ++i) {
-        const int u = i % C::kBufs;
-        const float s = s_next;
-        if (b + 1 < nkb) s_next = xs[(size_t)(b + 1) * a.lds] * ws[b + 1];
-        if (!__all_sync(0xffffffffu, mbar_wait_cluster(&acc_full[u], (i / C::kBufs) & 1, deadline, &abort_sh))) {
-          record_error_word(a.err, kErrTimeoutWord);
-          abort_sh = 1;
-          break;
+        const float s = x_next * ws.at(b, lane);
+        if (b + C::kAhead < nkb) prefetch_l1(xs + (size_t)C::kAhead * a.lds);
+        if (b + 1 < nkb) {
+          xs += a.lds;
+          x_next = *xs;
         }
-        tc_fence_after();
-        const uint32_t src = tmem + ((uint32_t)(sp * 32) << 16) + u * C::BN + half * 128;
-        uint32_t v[2][32];
-        tmem_ld32(src, v[0]);
+        const uint32_t buf = src + (i & 1) * C::BN;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {  // the next quarter loads while this one is added
+        for (int c = 0; c < 4; ++c) {  // the next piece loads while this one is added
           tmem_ld_wait();
-          if (c < 3) tmem_ld32(src + 32 * (c + 1), v[(c + 1) & 1]);
-          if (c == 3) {
+          if (c < 3) {
+            tmem_ld32(buf + 32 * (c + 1), v[(c + 1) & 1]);
+          } else {
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive_remote_relaxed(acc_empty_lead + (uint32_t)(u * sizeof(uint64_t)));
+            if (lane == 0) mbar_arrive_remote_relaxed(acc_empty_lead + (uint32_t)((i & 1) * sizeof(uint64_t)));
+            if (b + 1 < nkb || more) {
+              wait_block(i + 1);
+              tmem_ld32(src + ((i + 1) & 1) * C::BN, v[0]);
+            }
           }
 #pragma unroll
           for (int e = 0; e < 32; e += 2)
@@ -661,29 +708,35 @@ __global__ void __launch_bounds__(Pair::kThreads, 1)
                  s);
         }
       }
-      if (abort_sh) break;
-      const int rows = a.T - row0;
       const int col0 = nt * C::BN + half * 128;
-      if (rows > 0 && col0 < a.D) {
+      if (row0 < a.T && col0 < a.D && !abort_sh) {
+        uint32_t o[32];
+        if (lane == 0) bulk_wait_read_all();  // the last tile's stores have left the staging area
+        __syncwarp();
         if (a.out_f32) {
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            uint32_t o[32];
+            if (col0 + 32 * c >= a.D) break;
+            if (c == 2) {
+              if (lane == 0) bulk_wait_read_all();
+              __syncwarp();
+            }
 #pragma unroll
             for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(acc[32 * c + e]);
-            store_rows<1>(a, wst, o, row0, rows, col0 + 32 * c, lane);
+            put_rows<1>(a, &mapy, wst + (c & 1) * 4096, o, row0, col0 + 32 * c, lane);
           }
         } else {
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            uint32_t o[32];
+            if (col0 + 64 * c >= a.D) break;
 #pragma unroll
             for (int e = 0; e < 32; ++e) o[e] = pack_bf16x2(acc[64 * c + 2 * e], acc[64 * c + 2 * e + 1]);
-            store_rows<2>(a, wst, o, row0, rows, col0 + 64 * c, lane);
+            put_rows<2>(a, &mapy, wst + c * 4096, o, row0, col0 + 64 * c, lane);
           }
         }
       }
     }
+    if (lane == 0) bulk_wait_all();  // the stores are complete before the grid is
   }
   tc_fence_before();
   __syncthreads();
@@ -744,9 +797,12 @@ cudaError_t launch_linear(const uint8_t* x, const float* xs, int lds, int T, int
     static bool done[64] = {};
     cudaError_t e = opt_in_smem((const void*)fp8_pair_kernel, Pair::kSmemBytes, done);
     if (e != cudaSuccess) return e;
+    CUtensorMap my = mx;  // not used unless rows of Y start on 16-byte boundaries
+    if (a.vec_y && !rows_map(&my, y, (uint64_t)T, (uint64_t)D, (uint64_t)ldy, out_f32 ? 4 : 2, 32)) return cudaErrorInvalidValue;
+    void* pair_args[] = {&mx, &mw, &my, &a};
     const int pairs = (int)(pair_tiles < dev->sms / 2 ? pair_tiles : dev->sms / 2);
     return launch_pdl((const void*)fp8_pair_kernel, dim3(2 * pairs), dim3(Pair::kThreads), Pair::kSmemBytes, 2, stream,
-                      args);
+                      pair_args);
   }
   static bool done[64] = {};
   cudaError_t e = opt_in_smem((const void*)fp8_tile_kernel, Tile::kSmemBytes, done);
