@@ -106,6 +106,27 @@ __device__ __forceinline__ void mbar_arrive_cta(uint64_t* bar) {
   asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
+// Bounded wait without a clock: the number of tries is limited instead (each
+// takes 20 cycles or more, and up to about a microsecond while the phase is
+// open), which leaves no 64-bit deadline in registers.  70 cycles less a wait in
+// a loop that is short of them.
+__device__ __forceinline__ bool mbar_wait_short(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  for (uint32_t n = 0; !mbar_try_wait(bar, parity); ++n)
+    if (*abort || n == (1u << 27)) return false;
+  return true;
+}
+// whether the phase of parity `parity` is complete, without waiting for it
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
 // from shared memory of a CTA of the cluster
 __device__ __forceinline__ float ld_shared_cluster_f(uint32_t addr) {
   float v;

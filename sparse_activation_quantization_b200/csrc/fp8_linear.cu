@@ -444,12 +444,14 @@ __global__ void __launch_bounds__(Tile::kThreads, 1)
 //   warp 0      one thread copies: the CTA's own two boxes per 128-k block; their
 //               bytes count on the even CTA's barrier
 //   warp 1      TMEM allocation; in the even CTA one thread issues the MMAs into
-//               two 256-column TMEM buffers; its commits arrive on both CTAs'
-//               barriers
-// A block's four MMAs take about 520 cycles.  Adding its 256 columns takes each
-// warp scheduler 256 cycles of the FMA pipe, so everything else a sum warp does
-// per block has to hide behind that: a 32-column piece is read while the one
-// before is added, over the block's end as well, and the scales come ahead.
+//               four 128-column TMEM buffers, half a tile's columns each; its
+//               commits arrive on both CTAs' barriers
+// The MMAs of a block take about 520 cycles.  Adding its 256 columns takes each
+// warp scheduler 256 cycles of the FMA pipe, and the plain loop below (wait, read
+// 32 columns, add them) 390 in all, two warps taking turns.  (Reading the next
+// piece while one is added needs 192 registers of values alone and spills: 650.)
+// A buffer's way round (sums' release, across the pair, MMAs, commit, read) takes
+// more than 1200 cycles, so there are four of them.
 // Waits acquire at CTA scope: what they guard is TMEM (ordered by the tcgen05
 // fences) and bytes of the copy engine.  (At cluster scope a wait that need not
 // wait takes 250 cycles.)
@@ -462,9 +464,8 @@ struct Pair {
   static constexpr int BM = 256, BN = 256;
   static constexpr int kStages = 5;
   static constexpr int kStageBytes = 2 * 16384;
-  static constexpr int kBufs = 2;
+  static constexpr int kBufs = 4, kBufCols = 128;
   static constexpr int kSums = 8;  // warps
-  static constexpr int kAhead = 5;  // blocks that scales of X are brought near before they are due
   static constexpr int kThreads = 32 * (kSums + 4);
   static constexpr int kRegsLaunch = 168, kRegsSum = 224, kRegsOther = 56;
   static constexpr int kOffStage = kStages * kStageBytes;
@@ -617,27 +618,36 @@ __global__ void __launch_bounds__(Pair::kThreads, 1)
         }
     }
     if (warp == 1 && leader && elect_one()) {
-      constexpr uint32_t idesc = idesc_e4m3(C::BM, C::BN);
+      constexpr uint32_t idesc = idesc_e4m3(C::BM, C::kBufCols);
       int i = 0, s = 0;
       uint32_t phase = 0;
       for (int tile = pair; tile < ntiles && !abort_sh; tile += npairs) {
         const uint64_t deadline = globaltimer_ns() + kWaitNs;
         for (int b = 0; b < nkb; ++b, ++i) {
-          const int u = i & 1;
-          if (!mbar_wait(&full_bar[s], phase, deadline, &abort_sh) ||
-              (i >= C::kBufs && !mbar_wait(&acc_empty[u], ((i >> 1) & 1) ^ 1, deadline, &abort_sh))) {
+          const int u = (i & 1) * 2;
+          const uint32_t taken = ((i >> 1) & 1) ^ 1;
+          // the three answers are asked for at once; what is not there yet is waited for
+          const bool f = mbar_test(&full_bar[s], phase);
+          const bool e0 = mbar_test(&acc_empty[u], taken), e1 = mbar_test(&acc_empty[u + 1], taken);
+          bool ok = f || mbar_wait(&full_bar[s], phase, deadline, &abort_sh);
+          const uint32_t st = smem_u32(smem + s * C::kStageBytes);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {  // 64 of each CTA's columns of W
+            ok = ok && (i < 2 || (h ? e1 : e0) || mbar_wait(&acc_empty[u + h], taken, deadline, &abort_sh));
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              mma_f8_pair(tmem + (u + h) * C::kBufCols, smem_desc(st + 32 * j, 16, 1024, kSw128),
+                          smem_desc(st + 16384 + 8192 * h + 32 * j, 16, 1024, kSw128), idesc, j > 0);
+            tc_commit_pair_mc(&acc_full[u + h], 0x3);
+          }
+          if (!ok) {
             record_error_word(a.err, kErrTimeoutWord);
             abort_sh = 1;
             break;
           }
-          tc_fence_after();
-          const uint32_t st = smem_u32(smem + s * C::kStageBytes);
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            mma_f8_pair(tmem + u * C::BN, smem_desc(st + 32 * j, 16, 1024, kSw128),
-                        smem_desc(st + 16384 + 32 * j, 16, 1024, kSw128), idesc, j > 0);
           tc_commit_pair_mc(&empty_bar[s], 0x3);
-          tc_commit_pair_mc(&acc_full[u], 0x3);
           if (++s == C::kStages) {
             s = 0;
             phase ^= 1;
@@ -651,63 +661,75 @@ __global__ void __launch_bounds__(Pair::kThreads, 1)
     const uint32_t acc_empty_lead = mapa_shared(smem_u32(&acc_empty[0]), 0);
     uint8_t* wst = smem + C::kOffStage + (size_t)(warp - 4) * 8192;
     const int d_blocks = blocks_of(a.D);
-    const uint32_t src = tmem + ((uint32_t)(sp * 32) << 16) + half * 128;
-    uint64_t deadline = globaltimer_ns() + kWaitNs;
-    // Where a wait runs out the warp goes on as one, with sums that nobody stores.
-    auto wait_block = [&](int i) {
-      if (!mbar_wait(&acc_full[i & 1], (i >> 1) & 1, deadline, &abort_sh)) {
-        record_error_word(a.err, kErrTimeoutWord);
-        abort_sh = 1;
+    const uint32_t src = tmem + ((uint32_t)(sp * 32) << 16) + half * 64;
+    int n = 0;  // buffers taken
+    // Scales of the next four blocks, on their way while four are added: everything
+    // that goes through the load path is slow beside the MMAs' operand reads, and
+    // a load and a shuffle per block took 300 cycles of it.
+    constexpr int kGroup = 4;
+    const float *xs = nullptr, *ws = nullptr;
+    float nx[kGroup], nw[kGroup];
+    auto load_scales = [&](int b0) {
+#pragma unroll
+      for (int j = 0; j < kGroup; ++j) {
+        const int b = min(b0 + j, nkb - 1);
+        nx[j] = xs[(size_t)b * a.lds];
+        nw[j] = ws[b];
       }
-      __syncwarp();
-      tc_fence_after();
     };
-    int i = 0;
-    uint32_t v[2][32];
-    if (pair < ntiles) {
-      wait_block(0);
-      tmem_ld32(src, v[0]);
-    }
+    auto scales = [&](int tile) {
+      int mt, nt;
+      coords(tile, mt, nt);
+      xs = a.xs + min(mt * C::BM + (int)rank * 128 + sp * 32 + lane, a.T - 1);
+      ws = a.ws + (size_t)min(nt * 2 + half, d_blocks - 1) * nkb;
+      load_scales(0);
+    };
+    bool seen = false;  // the next buffer was full when it was asked for
+    if (pair < ntiles) scales(pair);
     for (int tile = pair; tile < ntiles && !abort_sh; tile += npairs) {
       int mt, nt;
       coords(tile, mt, nt);
-      const bool more = tile + npairs < ntiles;
-      deadline = globaltimer_ns() + kWaitNs;
       const int row0 = mt * C::BM + (int)rank * 128 + sp * 32;
-      const float* xs = a.xs + min(row0 + lane, a.T - 1);
-      ScaleRow ws;
-      ws.start(a.ws + (size_t)min(nt * 2 + half, d_blocks - 1) * nkb, nkb, 0, lane);
       float acc[128] = {};
-      float x_next = *xs;
-      for (int b = 1; b < C::kAhead && b < nkb; ++b) prefetch_l1(xs + (size_t)b * a.lds);
-      for (int b = 0; b < nkb; ++b, ++i) {
-        const float s = x_next * ws.at(b, lane);
-        if (b + C::kAhead < nkb) prefetch_l1(xs + (size_t)C::kAhead * a.lds);
-        if (b + 1 < nkb) {
-          xs += a.lds;
-          x_next = *xs;
-        }
-        const uint32_t buf = src + (i & 1) * C::BN;
+      for (int b0 = 0; b0 < nkb; b0 += kGroup) {
+        float s[kGroup];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {  // the next piece loads while this one is added
-          tmem_ld_wait();
-          if (c < 3) {
-            tmem_ld32(buf + 32 * (c + 1), v[(c + 1) & 1]);
-          } else {
-            tc_fence_before();
+        for (int j = 0; j < kGroup; ++j) s[j] = nx[j] * nw[j];
+        if (b0 + kGroup < nkb) load_scales(b0 + kGroup);
+#pragma unroll
+        for (int j = 0; j < kGroup; ++j) {
+          if (b0 + j >= nkb) break;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int u = n & 3;
+            // where a wait runs out the warp goes on as one, with sums that nobody stores
+            if (!seen && !mbar_wait_short(&acc_full[u], (n >> 2) & 1, &abort_sh)) {
+              record_error_word(a.err, kErrTimeoutWord);
+              abort_sh = 1;
+            }
+            ++n;
             __syncwarp();
-            if (lane == 0) mbar_arrive_remote_relaxed(acc_empty_lead + (uint32_t)((i & 1) * sizeof(uint64_t)));
-            if (b + 1 < nkb || more) {
-              wait_block(i + 1);
-              tmem_ld32(src + ((i + 1) & 1) * C::BN, v[0]);
+            tc_fence_after();
+#pragma unroll
+            for (int c = 0; c < 64; c += 32) {
+              uint32_t v[32];
+              tmem_ld32(src + u * C::kBufCols + c, v);
+              tmem_ld_wait();
+              if (c == 32) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_remote_relaxed(acc_empty_lead + (uint32_t)(u * sizeof(uint64_t)));
+                seen = mbar_test(&acc_full[n & 3], (n >> 2) & 1);  // answered while these are added
+              }
+#pragma unroll
+              for (int e = 0; e < 32; e += 2)
+                fma2(acc[64 * h + c + e], acc[64 * h + c + e + 1], __uint_as_float(v[e]), __uint_as_float(v[e + 1]),
+                     s[j]);
             }
           }
-#pragma unroll
-          for (int e = 0; e < 32; e += 2)
-            fma2(acc[32 * c + e], acc[32 * c + e + 1], __uint_as_float(v[c & 1][e]), __uint_as_float(v[c & 1][e + 1]),
-                 s);
         }
       }
+      if (tile + npairs < ntiles) scales(tile + npairs);  // on their way while this tile is stored
       const int col0 = nt * C::BN + half * 128;
       if (row0 < a.T && col0 < a.D && !abort_sh) {
         uint32_t o[32];

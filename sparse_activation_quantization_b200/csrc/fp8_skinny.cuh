@@ -122,7 +122,7 @@ struct ScaleRow {
   const float* p;  // the row of scales
   int n, base;
   float cur, ahead;
-  __device__ __forceinline__ float load(int b) const { return b < n ? __ldg(p + b) : 0.0f; }
+  __device__ __forceinline__ float load(int b) const { return b < n ? p[b] : 0.0f; }
   __device__ __forceinline__ void start(const float* row, int blocks, int b0, int lane) {
     p = row;
     n = blocks;
