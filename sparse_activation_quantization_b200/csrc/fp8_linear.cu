@@ -507,21 +507,22 @@ __device__ __forceinline__ void copy_rows(const LinearArgs& a, const uint8_t* ws
   }
   __syncwarp();
 }
-// 32 rows x 32 four-byte words of output through 4 KB of staging, which no store reads any more
-template <int kPer>
-__device__ __forceinline__ void put_rows(const LinearArgs& a, const CUtensorMap* mapy, uint8_t* wst,
-                                         const uint32_t (&v)[32], int row0, int col0, int lane) {
-  stage_rows(wst, v, lane);
+// Two staged pieces of 32 rows x 128 bytes, the second kSpan columns on, to Y
+template <int kPer, int kSpan>
+__device__ __forceinline__ void put_rows(const LinearArgs& a, const CUtensorMap* mapy, uint8_t* wst, int row0, int col0,
+                                         int lane) {
   if (a.vec_y) {
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) {
       tma_store_2d(mapy, wst, col0, row0);
+      if (col0 + kSpan < a.D) tma_store_2d(mapy, wst + 4096, col0 + kSpan, row0);
       bulk_commit_group();
     }
   } else {
     __syncwarp();
     copy_rows<kPer>(a, wst, row0, col0, lane);
+    if (col0 + kSpan < a.D) copy_rows<kPer>(a, wst + 4096, row0, col0 + kSpan, lane);
   }
 }
 
@@ -710,22 +711,17 @@ __global__ void __launch_bounds__(Pair::kThreads, 1)
             ++n;
             __syncwarp();
             tc_fence_after();
+            uint32_t v[64];
+            tmem_ld32(src + u * C::kBufCols, *reinterpret_cast<uint32_t(*)[32]>(&v[0]));
+            tmem_ld32(src + u * C::kBufCols + 32, *reinterpret_cast<uint32_t(*)[32]>(&v[32]));
+            tmem_ld_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_remote_relaxed(acc_empty_lead + (uint32_t)(u * sizeof(uint64_t)));
+            seen = mbar_test(&acc_full[n & 3], (n >> 2) & 1);  // answered while these are added
 #pragma unroll
-            for (int c = 0; c < 64; c += 32) {
-              uint32_t v[32];
-              tmem_ld32(src + u * C::kBufCols + c, v);
-              tmem_ld_wait();
-              if (c == 32) {
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_remote_relaxed(acc_empty_lead + (uint32_t)(u * sizeof(uint64_t)));
-                seen = mbar_test(&acc_full[n & 3], (n >> 2) & 1);  // answered while these are added
-              }
-#pragma unroll
-              for (int e = 0; e < 32; e += 2)
-                fma2(acc[64 * h + c + e], acc[64 * h + c + e + 1], __uint_as_float(v[e]), __uint_as_float(v[e + 1]),
-                     s[j]);
-            }
+            for (int e = 0; e < 64; e += 2)
+              fma2(acc[64 * h + e], acc[64 * h + e + 1], __uint_as_float(v[e]), __uint_as_float(v[e + 1]), s[j]);
           }
         }
       }
@@ -738,23 +734,24 @@ __global__ void __launch_bounds__(Pair::kThreads, 1)
         if (a.out_f32) {
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            if (col0 + 32 * c >= a.D) break;
             if (c == 2) {
+              if (col0 + 64 >= a.D) break;
               if (lane == 0) bulk_wait_read_all();
               __syncwarp();
             }
 #pragma unroll
             for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(acc[32 * c + e]);
-            put_rows<1>(a, &mapy, wst + (c & 1) * 4096, o, row0, col0 + 32 * c, lane);
+            stage_rows(wst + (c & 1) * 4096, o, lane);
+            if (c & 1) put_rows<1, 32>(a, &mapy, wst, row0, col0 + 32 * (c - 1), lane);
           }
         } else {
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            if (col0 + 64 * c >= a.D) break;
 #pragma unroll
             for (int e = 0; e < 32; ++e) o[e] = pack_bf16x2(acc[64 * c + 2 * e], acc[64 * c + 2 * e + 1]);
-            put_rows<2>(a, &mapy, wst + c * 4096, o, row0, col0 + 64 * c, lane);
+            stage_rows(wst + c * 4096, o, lane);
           }
+          put_rows<2, 64>(a, &mapy, wst, row0, col0, lane);
         }
       }
     }
