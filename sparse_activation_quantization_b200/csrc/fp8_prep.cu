@@ -26,24 +26,47 @@ struct PrepArgs {
   float eps;
 };
 
-// v of 8 consecutive columns before the norm; the residual form returns the
-// bf16-rounded sum and stores it
+// 8 consecutive columns as they lie in memory
 template <int kKind>
-__device__ __forceinline__ void load8(const PrepArgs& a, int t, int c, float (&v)[8]) {
-  unpack_bf16x8(*reinterpret_cast<const uint4*>(a.x + (size_t)t * a.ldx + c), v);
-  if (kKind == kPlain) return;
-  float w[8];
-  unpack_bf16x8(*reinterpret_cast<const uint4*>(a.b + (size_t)t * a.ldb + c), w);
-  if (kKind == kResidual) {
+struct Raw {
+  uint4 x, w;
+  __device__ __forceinline__ void load(const PrepArgs& a, int t, int c) {
+    x = *reinterpret_cast<const uint4*>(a.x + (size_t)t * a.ldx + c);
+    if (kKind != kPlain) w = *reinterpret_cast<const uint4*>(a.b + (size_t)t * a.ldb + c);
+  }
+  __device__ __forceinline__ void clear() { x = w = make_uint4(0u, 0u, 0u, 0u); }
+  // the residual form's sum, rounded to bf16; the other forms' x
+  __device__ __forceinline__ uint4 stream() const {
+    if (kKind != kResidual) return x;
+    float v[8], u[8];
+    unpack_bf16x8(x, v);
+    unpack_bf16x8(w, u);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] += w[i];
-    const uint4 h = pack_bf16x8(v);
-    if (a.h) *reinterpret_cast<uint4*>(a.h + (size_t)t * a.ldh + c) = h;
-    unpack_bf16x8(h, v);
-  } else {
+    for (int i = 0; i < 8; ++i) v[i] += u[i];
+    return pack_bf16x8(v);
+  }
+};
+__device__ __forceinline__ void store_stream(const PrepArgs& a, int t, int c, const uint4& h) {
+  if (a.h) *reinterpret_cast<uint4*>(a.h + (size_t)t * a.ldh + c) = h;
+}
+// v of 8 consecutive columns before the norm; the residual form stores the sum
+template <int kKind>
+__device__ __forceinline__ void values8(const PrepArgs& a, int t, int c, const Raw<kKind>& raw, float (&v)[8]) {
+  const uint4 h = raw.stream();
+  if (kKind == kResidual) store_stream(a, t, c, h);
+  unpack_bf16x8(h, v);
+  if (kKind == kSwiglu) {
+    float w[8];
+    unpack_bf16x8(raw.w, w);
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = silu_mul(v[i], w[i]);
   }
+}
+template <int kKind>
+__device__ __forceinline__ void load8(const PrepArgs& a, int t, int c, float (&v)[8]) {
+  Raw<kKind> raw;
+  raw.load(a, t, c);
+  values8<kKind>(a, t, c, raw, v);
 }
 
 // scale and codes of one 128-block that 16 neighbouring lanes hold, 8 values
@@ -65,23 +88,42 @@ __device__ __forceinline__ void quant8(const PrepArgs& a, int t, int c, const fl
   }
 }
 
-// Without a norm every 128-block stands alone: half a warp per block.
+// Without a norm every 128-block stands alone: half a warp per block, kUnroll
+// blocks on their way at once.  A thread steps through (row, block) by the grid's
+// step, split into rows and blocks once, so the loop divides nothing.
+constexpr int kUnroll = 4;
 template <int kKind>
 __global__ void __launch_bounds__(256) fp8_quant_kernel(const PrepArgs a) {
   pdl_trigger();
   pdl_wait();
   const int kb = blocks_of(a.K);
-  const long long total = (long long)a.T * kb;
-  const long long stride = (long long)gridDim.x * 16;
-  // the loop is uniform over the warp: both halves take part in the shuffles
-  for (long long i0 = (long long)blockIdx.x * 16 + (threadIdx.x >> 5) * 2; i0 < total; i0 += stride) {
-    const long long i = i0 + ((threadIdx.x >> 4) & 1);
-    const bool in = i < total;
-    const int t = in ? (int)(i / kb) : 0;
-    const int c = in ? (int)(i - (long long)t * kb) * kBlock + (threadIdx.x & 15) * 8 : a.K;
-    float v[8] = {};
-    if (c < a.K) load8<kKind>(a, t, c, v);
-    quant8(a, t, c, v);
+  const int step = (int)gridDim.x * 16, dt = step / kb, db = step - dt * kb;
+  const int i0 = (int)blockIdx.x * 16 + (int)(threadIdx.x >> 4);
+  int t = i0 / kb, b = i0 - t * kb;
+  const int lane_col = (threadIdx.x & 15) * 8;
+  // the loop is uniform over the warp, so both halves take part in the shuffles
+  while (__any_sync(0xffffffffu, t < a.T)) {
+    Raw<kKind> raw[kUnroll];
+    int rt[kUnroll], rc[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      rt[u] = t < a.T ? t : 0;
+      rc[u] = t < a.T ? b * kBlock + lane_col : a.K;
+      raw[u].clear();
+      if (rc[u] < a.K) raw[u].load(a, rt[u], rc[u]);
+      t = t < a.T ? t + dt : t;  // stays past the end without overflowing
+      b += db;
+      if (b >= kb) {
+        b -= kb;
+        ++t;
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      float v[8] = {};
+      if (rc[u] < a.K) values8<kKind>(a, rt[u], rc[u], raw[u], v);
+      quant8(a, rt[u], rc[u], v);
+    }
   }
 }
 
@@ -105,9 +147,9 @@ __device__ __noinline__ double inv_rms_wide(double s2, const PrepArgs& a) {
 }
 
 // With a norm, one CTA (or one warp) holds a row: R vectors of 8 columns per
-// thread.  kWarpRow: a warp per row, no barrier.
+// thread, as bf16.  kWarpRow: a warp per row, no barrier.
 template <int kKind, int R, bool kWarpRow>
-__global__ void __launch_bounds__(1024) fp8_norm_kernel(const PrepArgs a) {
+__global__ void __launch_bounds__(kWarpRow ? 256 : 1024) fp8_norm_kernel(const PrepArgs a) {
   __shared__ float part[32];
   pdl_trigger();
   pdl_wait();
@@ -116,19 +158,25 @@ __global__ void __launch_bounds__(1024) fp8_norm_kernel(const PrepArgs a) {
   const int me = kWarpRow ? lane : (int)threadIdx.x;
   const int t = kWarpRow ? (int)(blockIdx.x * (blockDim.x >> 5)) + warp : (int)blockIdx.x;
   if (kWarpRow && t >= a.T) return;
-  float v[R][8];
+  Raw<kKind> raw[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const int c = (r * nthr + me) * 8;
+    raw[r].clear();
+    if (c < a.K) raw[r].load(a, t, c);
+  }
+  uint4 h[R];
   float ss = 0.0f;
 #pragma unroll
   for (int r = 0; r < R; ++r) {
     const int c = (r * nthr + me) * 8;
+    h[r] = raw[r].stream();
+    if (kKind == kResidual && c < a.K) store_stream(a, t, c, h[r]);
+    float v[8];
+    unpack_bf16x8(h[r], v);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[r][i] = 0.0f;
-    if (c < a.K) load8<kKind>(a, t, c, v[r]);
+    for (int i = 0; i < 8; ++i) ss = fmaf(v[i], v[i], ss);
   }
-#pragma unroll
-  for (int r = 0; r < R; ++r)
-#pragma unroll
-    for (int i = 0; i < 8; ++i) ss = fmaf(v[r][i], v[r][i], ss);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
   if (!kWarpRow) {
@@ -139,33 +187,36 @@ __global__ void __launch_bounds__(1024) fp8_norm_kernel(const PrepArgs a) {
     for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
   }
   const float inv = __frsqrt_rn(__fadd_rn(__fdiv_rn(ss, (float)a.K), a.eps));
-  if (!square_sum_fits(ss)) {  // the same for every thread of the row
+  const bool fits = square_sum_fits(ss);  // the same for every thread of the row
+  double inv2 = 0.0;
+  if (!fits) {
     double s2 = 0.0;
 #pragma unroll
-    for (int r = 0; r < R; ++r)
+    for (int r = 0; r < R; ++r) {
+      float v[8];
+      unpack_bf16x8(h[r], v);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) s2 += (double)v[r][i] * (double)v[r][i];
-    const double inv2 = inv_rms_wide<kWarpRow>(s2, a);
-#pragma unroll
-    for (int r = 0; r < R; ++r)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[r][i] = (float)((double)v[r][i] * inv2);
-  } else {
-#pragma unroll
-    for (int r = 0; r < R; ++r)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[r][i] *= inv;
+      for (int i = 0; i < 8; ++i) s2 += (double)v[i] * (double)v[i];
+    }
+    inv2 = inv_rms_wide<kWarpRow>(s2, a);
   }
 #pragma unroll
   for (int r = 0; r < R; ++r) {
     const int c = (r * nthr + me) * 8;
+    float v[8];
+    unpack_bf16x8(h[r], v);
     if (c < a.K) {
       float g[8];
       unpack_bf16x8(*reinterpret_cast<const uint4*>(a.gamma + c), g);
+      if (fits) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[r][i] *= g[i];
+        for (int i = 0; i < 8; ++i) v[i] = v[i] * inv * g[i];
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = (float)((double)v[i] * inv2) * g[i];
+      }
     }
-    quant8(a, t, c, v[r]);
+    quant8(a, t, c, v);
   }
 }
 
@@ -234,25 +285,29 @@ cudaError_t launch_norm(PrepArgs& a, int grid, int block, cudaStream_t stream) {
 template <int kKind>
 cudaError_t launch_kind(PrepArgs& a, cudaStream_t stream) {
   void* args[] = {&a};
+  const Device* d = device();
+  if (!d) return cudaErrorInvalidDevice;
   if (!a.gamma) {
-    const Device* d = device();
-    if (!d) return cudaErrorInvalidDevice;
-    const long long want = ((long long)a.T * blocks_of(a.K) + 15) / 16;
-    const long long most = (long long)d->sms * 8;
-    return launch_pdl((const void*)fp8_quant_kernel<kKind>, dim3((unsigned)(want < most ? want : most)), dim3(256), 0,
-                      1, stream, args);
-  }
-  if (a.K <= 1024) {
-    const int rows = 4;
-    const int grid = (a.T + rows - 1) / rows;
-    if (a.K <= 256) return launch_norm<kKind, 1, true>(a, grid, 32 * rows, stream);
-    if (a.K <= 512) return launch_norm<kKind, 2, true>(a, grid, 32 * rows, stream);
-    return launch_norm<kKind, 4, true>(a, grid, 32 * rows, stream);
+    // 16 blocks a CTA and step, kUnroll steps at once where that still fills the GPU
+    const long long want = ((long long)a.T * blocks_of(a.K) + 15) / 16, fill = (long long)d->sms * 4;
+    long long grid = (want + kUnroll - 1) / kUnroll;
+    grid = grid < fill ? (want < fill ? want : fill) : (grid < 2 * fill ? grid : 2 * fill);
+    return launch_pdl((const void*)fp8_quant_kernel<kKind>, dim3((unsigned)grid), dim3(256), 0, 1, stream, args);
   }
   const int vecs = (a.K + 7) / 8;
+  // A warp per row where there are rows enough for 8 warps on every SM, or where a row is short.
+  if (vecs <= 128 || (vecs <= 512 && a.T >= 8 * d->sms)) {
+    const int rows = 4, grid = (a.T + rows - 1) / rows;
+    if (vecs <= 32) return launch_norm<kKind, 1, true>(a, grid, 32 * rows, stream);
+    if (vecs <= 64) return launch_norm<kKind, 2, true>(a, grid, 32 * rows, stream);
+    if (vecs <= 128) return launch_norm<kKind, 4, true>(a, grid, 32 * rows, stream);
+    if (vecs <= 256) return launch_norm<kKind, 8, true>(a, grid, 32 * rows, stream);
+    return launch_norm<kKind, 16, true>(a, grid, 32 * rows, stream);
+  }
+  // A CTA per row: a vector per thread while the rows do not fill the GPU, else four, so that several rows are on
+  // their way on an SM.
   auto block = [&](int r) { return ((vecs + r - 1) / r + 31) / 32 * 32; };
-  if (vecs <= 1024) return launch_norm<kKind, 1, false>(a, a.T, block(1), stream);
-  if (vecs <= 2048) return launch_norm<kKind, 2, false>(a, a.T, block(2), stream);
+  if (vecs <= 1024 && a.T <= d->sms) return launch_norm<kKind, 1, false>(a, a.T, block(1), stream);
   if (vecs <= 4096) return launch_norm<kKind, 4, false>(a, a.T, block(4), stream);
   return launch_pdl((const void*)fp8_norm_long_kernel<kKind>, dim3(a.T), dim3(1024), 0, 1, stream, args);
 }
@@ -260,12 +315,33 @@ cudaError_t launch_kind(PrepArgs& a, cudaStream_t stream) {
 // --------------------------------------------------------------- weights ---
 
 // One 128 x 128 block of W [K][D] per CTA: amax, then codes transposed to
-// [D][K] through shared memory.  Thread (o, kg) holds columns 8 o .. 8 o + 7 of
-// rows 8 kg .. 8 kg + 7.  Shared memory holds row d as 16 chunks of 8 k-bytes,
-// chunk kg at kg ^ (d / 8), so that neither side meets bank conflicts.
-template <bool kVec>
+// [D][K] through shared memory.  Thread (o, kg) holds rows 8 kg .. 8 kg + 7 and
+// 8 columns of each, as 8 / kW loads of kW neighbouring columns (what D and the
+// base allow to be aligned): column 16 kW p + kW o + i.  Shared memory holds row
+// d as 16 chunks of 8 k-bytes, chunk kg at kg ^ (d / kW % 16), so that neither
+// side meets bank conflicts.
+template <int kW>
+struct PackVec;
+template <>
+struct PackVec<8> {
+  using type = uint4;
+};
+template <>
+struct PackVec<4> {
+  using type = uint2;
+};
+template <>
+struct PackVec<2> {
+  using type = uint32_t;
+};
+template <>
+struct PackVec<1> {
+  using type = uint16_t;
+};
+template <int kW>
 __global__ void __launch_bounds__(256) fp8_pack_kernel(const __nv_bfloat16* W, int K, int D, uint8_t* codes,
                                                        float* scales) {
+  using Vec = typename PackVec<kW>::type;
   __shared__ __align__(16) uint8_t tile[128 * 128];
   __shared__ float part[8];
   pdl_trigger();
@@ -273,28 +349,26 @@ __global__ void __launch_bounds__(256) fp8_pack_kernel(const __nv_bfloat16* W, i
   const int kb = blockIdx.x, db = blockIdx.y;
   const size_t e = blockIdx.z;
   const int o = threadIdx.x & 15, kg = threadIdx.x >> 4;
-  const int d0 = db * 128 + o * 8, k0 = kb * 128 + kg * 8;
+  const int d0 = db * 128, k0 = kb * 128 + kg * 8;
   const __nv_bfloat16* src = W + (e * K + k0) * (size_t)D + d0;
-  float v[8][8];
-  float m = 0.0f;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[j][i] = 0.0f;
-    if (k0 + j < K) {
-      if (kVec) {
-        if (d0 < D) unpack_bf16x8(*reinterpret_cast<const uint4*>(src + (size_t)j * D), v[j]);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (d0 + i < D) v[j][i] = __bfloat162float(src[(size_t)j * D + i]);
-      }
-    }
-  }
+  union {
+    Vec v[8 / kW];
+    uint16_t b[8];
+  } raw[8];  // [row]: bf16 of the thread's 8 columns
 #pragma unroll
   for (int j = 0; j < 8; ++j)
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(v[j][i]));
+    for (int p = 0; p < 8 / kW; ++p) {
+      const int c = (16 * p + o) * kW;
+      raw[j].v[p] = Vec{};
+      if (k0 + j < K && d0 + c < D) raw[j].v[p] = *reinterpret_cast<const Vec*>(src + (size_t)j * D + c);
+    }
+  auto value = [&](int j, int i) { return __uint_as_float((uint32_t)raw[j].b[i] << 16); };
+  float m = 0.0f;
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(value(j, i)));
 #pragma unroll
   for (int s = 16; s > 0; s >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, s));
   if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = m;
@@ -307,20 +381,21 @@ __global__ void __launch_bounds__(256) fp8_pack_kernel(const __nv_bfloat16* W, i
   if (threadIdx.x == 0) scales[(e * gridDim.y + db) * gridDim.x + kb] = s;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
+    const int d = (16 * (i / kW) + o) * kW + i % kW;
     uint2 q;
-    q.x = e4m3x4(v[0][i] * inv, v[1][i] * inv, v[2][i] * inv, v[3][i] * inv);
-    q.y = e4m3x4(v[4][i] * inv, v[5][i] * inv, v[6][i] * inv, v[7][i] * inv);
-    *reinterpret_cast<uint2*>(tile + (o * 8 + i) * 128 + ((kg ^ o) << 3)) = q;
+    q.x = e4m3x4(value(0, i) * inv, value(1, i) * inv, value(2, i) * inv, value(3, i) * inv);
+    q.y = e4m3x4(value(4, i) * inv, value(5, i) * inv, value(6, i) * inv, value(7, i) * inv);
+    *reinterpret_cast<uint2*>(tile + d * 128 + ((kg ^ o) << 3)) = q;
   }
   __syncthreads();
   const int q = threadIdx.x & 7;  // 16-byte chunk of the output row
 #pragma unroll
   for (int it = 0; it < 4; ++it) {
     const int r = it * 32 + (threadIdx.x >> 3);
-    const int ro = r >> 3;
+    const int ro = (r / kW) & 15;
     uint4 w = *reinterpret_cast<const uint4*>(tile + r * 128 + (((2 * q) ^ (ro & ~1)) << 3));
     if (ro & 1) w = make_uint4(w.z, w.w, w.x, w.y);
-    const int d = db * 128 + r, k = kb * 128 + q * 16;
+    const int d = d0 + r, k = kb * 128 + q * 16;
     if (d < D && k < K) *reinterpret_cast<uint4*>(codes + (e * D + d) * (size_t)K + k) = w;
   }
 }
@@ -353,9 +428,13 @@ cudaError_t launch_prep(int kind, const void* x, long long ldx, const void* b, l
 cudaError_t launch_pack(const void* W, int K, int D, int E, uint8_t* codes, float* scales, cudaStream_t stream) {
   const __nv_bfloat16* w = static_cast<const __nv_bfloat16*>(W);
   void* args[] = {&w, &K, &D, &codes, &scales};
-  const bool vec = D % 8 == 0 && reinterpret_cast<uintptr_t>(W) % 16 == 0;
-  return launch_pdl(vec ? (const void*)fp8_pack_kernel<true> : (const void*)fp8_pack_kernel<false>,
-                    dim3(blocks_of(K), blocks_of(D), E), dim3(256), 0, 1, stream, args);
+  // the widest load that every row's start allows
+  const uintptr_t at = reinterpret_cast<uintptr_t>(W) | (uintptr_t)D * 2;
+  const void* k = at % 16 == 0  ? (const void*)fp8_pack_kernel<8>
+                  : at % 8 == 0 ? (const void*)fp8_pack_kernel<4>
+                  : at % 4 == 0 ? (const void*)fp8_pack_kernel<2>
+                                : (const void*)fp8_pack_kernel<1>;
+  return launch_pdl(k, dim3(blocks_of(K), blocks_of(D), E), dim3(256), 0, 1, stream, args);
 }
 
 }  // namespace fp8
