@@ -20,11 +20,17 @@ constexpr int kErrTimeoutWord = -5;          // SHARQ_ERR_TIMEOUT
 
 __host__ __device__ __forceinline__ int blocks_of(int n) { return (n + kBlock - 1) / kBlock; }
 
-// s = max / 448, at least the smallest normal float (so 1/s is finite), 1 for
-// a block of zeros.  A NaN in the block is skipped by the maximum and keeps
-// its own code; an infinity makes s infinite and the block NaN.
+// s = max / 448 to nearest, at least the smallest normal float (so 1/s is
+// finite), 1 for a block of zeros.  The quotient by Markstein's correction: q =
+// max y with y = 1/448 to nearest, then q + (max - 448 q) y, whose remainder an
+// FMA gives exactly.  (Where q is below the normal numbers the maximum takes
+// over.)  A NaN in the block is skipped by the maximum and keeps its own code; an
+// infinity makes s infinite and the block NaN.
 __device__ __forceinline__ float block_scale_e4m3(float amax) {
-  return amax > 0.0f ? fmaxf(__fdiv_rn(amax, kE4m3Max), 0x1p-126f) : 1.0f;
+  constexpr float y = 1.0f / kE4m3Max;
+  const float q = amax * y;
+  const float s = fmaxf(fmaf(fmaf(-kE4m3Max, q, amax), y, q), 0x1p-126f);
+  return amax > 0.0f ? (amax < INFINITY ? s : amax) : 1.0f;
 }
 
 // four floats -> four E4M3 bytes, a in the lowest (round to nearest even,
