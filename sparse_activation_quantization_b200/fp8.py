@@ -28,39 +28,37 @@ def _blocks(n):
     return -(-n // 128)
 
 
+# The handle of a device's current stream and the current device, without building a Stream object (3 us of a call)
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
+
+
+def _elsewhere(device, stream):
+    """whether a call has to enter another device or stream first"""
+    return stream is not None or _current_device() != device.index
+
+
 @contextlib.contextmanager
-def _other(device, stream):
-    with torch.cuda.device(device):
-        if stream is None:
-            yield torch.cuda.current_stream(device).cuda_stream
-        else:
-            with torch.cuda.stream(stream):
-                yield stream.cuda_stream
-
-
-class _here:
-    """the common case of _on: current device, current stream"""
-
-    __slots__ = ("ptr",)
-
-    def __init__(self, ptr):
-        self.ptr = ptr
-
-    def __enter__(self):
-        return self.ptr
-
-    def __exit__(self, *exc):
-        return False
-
-
 def _on(device, stream):
-    """Context in which a call's allocations and launches belong to `device`
-    and `stream`; gives the stream's handle."""
-    if stream is None and torch.cuda.current_device() == device.index:
-        return _here(torch.cuda.current_stream().cuda_stream)
+    """Context in which a call's allocations and launches belong to `device` and `stream` (None: its current one)."""
     if stream is not None and stream.device != device:
         raise ValueError(f"stream of {stream.device}, tensors on {device}")
-    return _other(device, stream)
+    with torch.cuda.device(device):
+        if stream is None:
+            yield
+        else:
+            with torch.cuda.stream(stream):
+                yield
+
+
+def _call(name, device, stream, *args):
+    """the sharq function `name` with these arguments and the stream's handle"""
+    if _elsewhere(device, stream):
+        with _on(device, stream):
+            return _call(name, device, None, *args)
+    status = getattr(_sq.lib(), name)(*args, _raw_stream(device.index))
+    if status != 0:
+        raise _sq.SharqError(status, name)
 
 
 def _cuda(name, t, dtype, device=None):
@@ -70,21 +68,23 @@ def _cuda(name, t, dtype, device=None):
         raise ValueError(f"{name} is on {t.device}, expected {device}")
 
 
-def _rows(name, t, shape, dtype, device=None):
+def _rows(name, t, shape, dtype, device):
     """(pointer, row stride) of a 2-D tensor whose rows are contiguous"""
-    _cuda(name, t, dtype, device)
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == device.index):
+        _cuda(name, t, dtype, device)
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    ld = t.stride(0) if shape[0] > 1 else shape[1]
-    if shape[1] > 1 and t.stride(1) != 1:
+    ld, step = t.stride()
+    if step != 1 and shape[1] > 1:
         raise ValueError(f"{name} must have contiguous rows")
-    return t.data_ptr(), ld
+    return t.data_ptr(), ld if shape[0] > 1 else shape[1]
 
 
 def _vector(name, t, n, dtype, device):
     if t is None:
         return None
-    _cuda(name, t, dtype, device)
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == device.index):
+        _cuda(name, t, dtype, device)
     if t.shape != (n,) or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous vector of {n}")
     return t.data_ptr()
@@ -110,12 +110,17 @@ class Fp8Weight:
         if _sq.sharq_fp8_weight_bytes(K, D, E) == 0:
             raise _sq.SharqError(-2, "sharq_fp8_weight_bytes")
         lead = () if W.dim() == 2 else (E,)
-        with _on(W.device, stream) as s:
-            W = W.contiguous()
-            codes = torch.empty((*lead, D, K), dtype=_F8, device=W.device)
-            scales = torch.empty((*lead, _blocks(D), _blocks(K)), dtype=torch.float32, device=W.device)
-            self._set(codes, scales, E, K, D)
-            _sq.sharq_fp8_pack_weight(W.data_ptr(), self.view, s)
+        if _elsewhere(W.device, stream):
+            with _on(W.device, stream):
+                self._pack(W, lead, E, K, D)
+        else:
+            self._pack(W, lead, E, K, D)
+
+    def _pack(self, W, lead, E, K, D):
+        W = W.contiguous()
+        self._set(W.new_empty((*lead, D, K), dtype=_F8),
+                  W.new_empty((*lead, _blocks(D), _blocks(K)), dtype=torch.float32), E, K, D)
+        _call("sharq_fp8_pack_weight", self.device, None, W.data_ptr(), self._ref)
 
     def _set(self, codes, scales, E, K, D):
         self.codes, self.scales = codes, scales
@@ -188,8 +193,7 @@ class Fp8Act:
         """Quantize X (bf16 [T, K]), normalised by its RMS when gamma is given."""
         x, ldx = _rows("X", X, (self.T, self.K), torch.bfloat16, self.device)
         g = _vector("gamma", gamma, self.K, torch.bfloat16, self.device)
-        with _on(self.device, stream) as s:
-            _sq._check(_sq.lib().sharq_fp8_prep(x, ldx, g, eps, self._ref, s), "sharq_fp8_prep")
+        _call("sharq_fp8_prep", self.device, stream, x, ldx, g, eps, self._ref)
         return self
 
     def prep_residual(self, X, res, res_out=None, gamma=None, eps=1e-5, stream=None):
@@ -200,9 +204,7 @@ class Fp8Act:
         r, ldr = _rows("res", res, shape, torch.bfloat16, self.device)
         o, ldo = _rows("res_out", res_out, shape, torch.bfloat16, self.device) if res_out is not None else (None, 0)
         g = _vector("gamma", gamma, self.K, torch.bfloat16, self.device)
-        with _on(self.device, stream) as s:
-            _sq._check(_sq.lib().sharq_fp8_prep_residual(x, ldx, r, ldr, o, ldo, g, eps, self._ref, s),
-                       "sharq_fp8_prep_residual")
+        _call("sharq_fp8_prep_residual", self.device, stream, x, ldx, r, ldr, o, ldo, g, eps, self._ref)
         return self
 
     def prep_silu_mul(self, gate, up, stream=None):
@@ -210,8 +212,7 @@ class Fp8Act:
         shape = (self.T, self.K)
         g, ldg = _rows("gate", gate, shape, torch.bfloat16, self.device)
         u, ldu = _rows("up", up, shape, torch.bfloat16, self.device)
-        with _on(self.device, stream) as s:
-            _sq._check(_sq.lib().sharq_fp8_prep_silu_mul(g, ldg, u, ldu, self._ref, s), "sharq_fp8_prep_silu_mul")
+        _call("sharq_fp8_prep_silu_mul", self.device, stream, g, ldg, u, ldu, self._ref)
         return self
 
 
@@ -242,8 +243,8 @@ class Fp8Workspace:
 
     def check(self, stream=None):
         """Synchronises and returns the error word of the calls that used it (0: none)."""
-        with _on(self.buf.device, stream) as s:
-            return _sq.sharq_check_status(self.ptr, s)
+        with _on(self.buf.device, stream):
+            return _sq.sharq_check_status(self.ptr, _raw_stream(self.buf.device.index))
 
 
 def _workspace(ws, device):
@@ -257,20 +258,21 @@ def fp8_linear(act, weight, out_dtype=None, out=None, ws=None, stream=None):
     (bf16 or float32, rows contiguous) may be a column slice of a wider tensor."""
     if weight.device != act.device:
         raise ValueError(f"weight on {weight.device}, activation on {act.device}")
+    device = act.device
+    if _elsewhere(device, stream):
+        with _on(device, stream):
+            return fp8_linear(act, weight, out_dtype, out, ws)
     out_dtype = out_dtype or (out.dtype if out is not None else torch.bfloat16)
     if out_dtype not in (torch.bfloat16, torch.float32):
         raise TypeError("the output is bf16 or float32")
-    code = _sq.SHARQ_OUT_F32 if out_dtype == torch.float32 else _sq.SHARQ_OUT_BF16
-    with _on(act.device, stream) as s:
-        if out is None:
-            out = torch.empty((act.T, weight.D), dtype=out_dtype, device=act.device)
-            y, ldy = out.data_ptr(), weight.D
-        else:
-            y, ldy = _rows("out", out, (act.T, weight.D), out_dtype, act.device)
-        ws = _workspace(ws, act.device) if ws is not None else \
-            Fp8Workspace.for_linear(act.T, act.K, weight.D, act.device)
-        _sq._check(_sq.lib().sharq_fp8_linear(act._ref, weight._ref, y, ldy, code, ws.ptr, ws.nbytes, s),
-                   "sharq_fp8_linear")
+    if out is None:
+        out = act.codes.new_empty((act.T, weight.D), dtype=out_dtype)
+        y, ldy = out.data_ptr(), weight.D
+    else:
+        y, ldy = _rows("out", out, (act.T, weight.D), out_dtype, device)
+    ws = _workspace(ws, device) if ws is not None else Fp8Workspace.for_linear(act.T, act.K, weight.D, device)
+    _call("sharq_fp8_linear", device, None, act._ref, weight._ref, y, ldy,
+          _sq.SHARQ_OUT_F32 if out_dtype == torch.float32 else _sq.SHARQ_OUT_BF16, ws.ptr, ws.nbytes)
     return out
 
 
@@ -286,22 +288,23 @@ def fp8_moe(x, logits, w13, w2, topk, renormalize=True, out=None, ws=None, retur
         raise ValueError(f"w2 on {w2.device}, w13 on {device}")
     if not isinstance(x, torch.Tensor) or x.dim() != 2:
         raise ValueError("x must be [T, H]")
+    if _elsewhere(device, stream):
+        with _on(device, stream):
+            return fp8_moe(x, logits, w13, w2, topk, renormalize, out, ws, return_routing)
     T = x.shape[0]
-    xp, ldx = _rows("x", x, (T, w13.K), torch.bfloat16, device)
+    shape = (T, w13.K)
+    xp, ldx = _rows("x", x, shape, torch.bfloat16, device)
     lp, ldl = _rows("logits", logits, (T, w13.E), torch.float32, device)
-    with _on(device, stream) as s:
-        if out is None:
-            out = torch.empty((T, w13.K), dtype=torch.bfloat16, device=device)
-            yp, ldy = out.data_ptr(), w13.K
-        else:
-            yp, ldy = _rows("out", out, (T, w13.K), torch.bfloat16, device)
-        ids = weights = None
-        if return_routing:
-            ids = torch.empty((T, topk), dtype=torch.int32, device=device)
-            weights = torch.empty((T, topk), dtype=torch.float32, device=device)
-        ws = _workspace(ws, device) if ws is not None else Fp8Workspace.for_moe(T, topk, w13, w2, device)
-        _sq._check(_sq.lib().sharq_fp8_moe(
-            xp, ldx, lp, ldl, T, topk, 1 if renormalize else 0, w13._ref, w2._ref, yp, ldy,
-            ids.data_ptr() if ids is not None else None, weights.data_ptr() if weights is not None else None,
-            ws.ptr, ws.nbytes, s), "sharq_fp8_moe")
+    if out is None:
+        out = x.new_empty(shape)
+        yp, ldy = out.data_ptr(), w13.K
+    else:
+        yp, ldy = _rows("out", out, shape, torch.bfloat16, device)
+    ids = weights = ip = pp = None
+    if return_routing:
+        ids, weights = x.new_empty((T, topk), dtype=torch.int32), logits.new_empty((T, topk))
+        ip, pp = ids.data_ptr(), weights.data_ptr()
+    ws = _workspace(ws, device) if ws is not None else Fp8Workspace.for_moe(T, topk, w13, w2, device)
+    _call("sharq_fp8_moe", device, None, xp, ldx, lp, ldl, T, topk, 1 if renormalize else 0, w13._ref, w2._ref, yp, ldy,
+          ip, pp, ws.ptr, ws.nbytes)
     return (out, ids, weights) if return_routing else out
