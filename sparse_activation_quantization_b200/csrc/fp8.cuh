@@ -254,6 +254,15 @@ struct Device {
 const Device* device();
 // a kernel's attribute that is set once per device: `done` is the kernel's own table
 cudaError_t opt_in_smem(const void* kernel, int bytes, bool (&done)[64]);
+// How many clusters of a kernel reside on the device at once, one CTA to an SM, asked once per device and cluster
+// size: `known` is the kernel's own table.  SMs lie in groups of unequal size, and a cluster needs one group, so fewer
+// may fit than the number of SMs says (15 of 8 on 148 SMs, 33 of 4); one that has to wait for a second wave doubles a
+// short kernel's time.  (The query counts one CTA per SM for a kernel that allocates TMEM; where two reside, twice as
+// many clusters do.)  0: could not be asked.
+struct Resident {
+  int n[64][9] = {};
+};
+int resident_clusters(const void* kernel, int threads, int smem, int cluster, Resident& known);
 // launch with programmatic dependence on the preceding kernel, and a cluster along x
 cudaError_t launch_pdl(const void* kernel, dim3 grid, dim3 block, int smem, int cluster, cudaStream_t stream,
                        void** args);

@@ -49,6 +49,32 @@ cudaError_t opt_in_smem(const void* kernel, int bytes, bool (&done)[64]) {
   return e;
 }
 
+int resident_clusters(const void* kernel, int threads, int smem, int cluster, Resident& known) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices || cluster < 1 || cluster > 8) return 0;
+  int& n = known.n[dev][cluster];
+  if (n == 0) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)cluster);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)cluster;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int got = 0;
+    if (cudaOccupancyMaxActiveClusters(&got, kernel, &cfg) != cudaSuccess) {
+      cudaGetLastError();
+      return 0;
+    }
+    n = got;
+  }
+  return n;
+}
+
 cudaError_t launch_pdl(const void* kernel, dim3 grid, dim3 block, int smem, int cluster, cudaStream_t stream,
                        void** args) {
   cudaLaunchConfig_t cfg = {};

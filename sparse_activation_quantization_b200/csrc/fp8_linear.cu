@@ -59,6 +59,24 @@ __device__ __forceinline__ void store_cols4(const LinearArgs& a, int row, int co
   }
 }
 
+// Sum in rank order of four floats at the same place of S <= 8 CTAs' shared
+// memory; every load is on its way before the first sum.
+__device__ __forceinline__ float4 sum_over_cluster(uint32_t addr, int S) {
+  float4 o[8], v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+  for (int p = 0; p < 8; ++p)
+    if (p < S) o[p] = ld_shared_cluster_f4(mapa_shared(addr, (uint32_t)p));
+#pragma unroll
+  for (int p = 0; p < 8; ++p)
+    if (p < S) {
+      v.x += o[p].x;
+      v.y += o[p].y;
+      v.z += o[p].z;
+      v.w += o[p].w;
+    }
+  return v;
+}
+
 // ------------------------------------------------------------ skinny form ---
 // 128 weight rows per CTA (or per cluster of S CTAs that share its K) against
 // all rows of X at once, as fp8_skinny.cuh describes.
@@ -205,14 +223,7 @@ __global__ void __launch_bounds__(Skinny<kN>::kThreads, 2)
     const int total = a.T * (kUnitRows / 4);
     const int i1 = (rank + 1) * total / S;
     for (int i = rank * total / S + (int)threadIdx.x; i < i1 && !bars.abort; i += C::kThreads) {
-      float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      for (int p = 0; p < S; ++p) {
-        const float4 o = ld_shared_cluster_f4(mapa_shared(base + i * 16, (uint32_t)p));
-        v.x += o.x;
-        v.y += o.y;
-        v.z += o.z;
-        v.w += o.w;
-      }
+      const float4 v = sum_over_cluster(base + i * 16, S);
       store_cols4(a, i / (kUnitRows / 4), first * kUnitRows + i % (kUnitRows / 4) * 4, v);
     }
     cluster_sync_all();  // no CTA leaves while a peer reads its sums
@@ -236,13 +247,15 @@ cudaError_t launch_skinny(LinearArgs& a, const Device* dev, cudaStream_t stream)
   cudaError_t e = opt_in_smem((const void*)fp8_skinny_kernel<kN>, C::kSmemBytes, done);
   if (e != cudaSuccess) return e;
   const int tiles = (a.D + kUnitRows - 1) / kUnitRows, most = 2 * dev->sms, nkb = blocks_of(a.K);
-  // A CTA per SM; a second one where each then still has 16 units or more.  Measured: 28 tiles of 148 blocks
-  // 15.8 us at one, 14.5 at two; 36 tiles of 28 blocks 6.5 and 9.9.
-  int s = most / tiles;
-  if (s > 8) s = 8;
-  if (s * tiles > dev->sms && nkb < 16 * s) s = dev->sms / tiles;
-  s = s < 1 ? 1 : s;
-  a.splits = s < nkb ? s : nkb;
+  // The widest cluster with which all reside at once: a CTA per SM, or a second one where each then still has 16
+  // units or more.  Measured: 28 tiles of 148 blocks 15.8 us at one, 14.5 at two; 36 tiles of 28 blocks 6.5 and 9.9.
+  static Resident known;
+  int s = 8;
+  for (; s > 1; --s) {
+    if (s > nkb || s * tiles > (nkb >= 16 * s ? most : dev->sms)) continue;
+    if (2 * resident_clusters((const void*)fp8_skinny_kernel<kN>, C::kThreads, C::kSmemBytes, s, known) >= tiles) break;
+  }
+  a.splits = s;
   void* args[] = {&mx, &mw, &a};
   const int grid = a.splits > 1 ? tiles * a.splits : (tiles < most ? tiles : most);
   return launch_pdl((const void*)fp8_skinny_kernel<kN>, dim3(grid), dim3(C::kThreads), C::kSmemBytes, a.splits, stream,
@@ -414,14 +427,7 @@ __global__ void __launch_bounds__(Tile::kThreads, 1)
       if (S == 1) {
         v = *reinterpret_cast<const float4*>(smem + (size_t)r * C::kRowFloats * 4 + lane * 16);
       } else {
-        v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        for (int p = 0; p < S; ++p) {
-          const float4 o = ld_shared_cluster_f4(mapa_shared(base + r * C::kRowFloats * 4, (uint32_t)p));
-          v.x += o.x;
-          v.y += o.y;
-          v.z += o.z;
-          v.w += o.w;
-        }
+        v = sum_over_cluster(base + r * C::kRowFloats * 4, S);
       }
       store_cols4(a, mt * C::BM + r, nt * C::BN + lane * 4, v);
     }
@@ -827,9 +833,14 @@ cudaError_t launch_linear(const uint8_t* x, const float* xs, int lds, int T, int
   cudaError_t e = opt_in_smem((const void*)fp8_tile_kernel, Tile::kSmemBytes, done);
   if (e != cudaSuccess) return e;
   const long long tiles = (long long)((T + 127) / 128) * ((D + 127) / 128);
-  int s = (int)(dev->sms / tiles);
-  s = s < 1 ? 1 : (s > 8 ? 8 : s);
-  a.splits = s < nkb ? s : nkb;
+  // the widest cluster with which all reside at once
+  static Resident known;
+  int s = 8;
+  for (; s > 1; --s) {
+    if (s > nkb || s * tiles > dev->sms) continue;
+    if (resident_clusters((const void*)fp8_tile_kernel, Tile::kThreads, Tile::kSmemBytes, s, known) >= tiles) break;
+  }
+  a.splits = s;
   return launch_pdl((const void*)fp8_tile_kernel, dim3(a.splits, (D + 127) / 128, (T + 127) / 128),
                     dim3(Tile::kThreads), Tile::kSmemBytes, a.splits, stream, args);
 }

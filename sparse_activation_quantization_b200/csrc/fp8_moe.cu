@@ -895,12 +895,19 @@ cudaError_t launch_form(MoeArgs& a, const uint8_t* w13, const uint8_t* w2, const
                  U::kSmemBytes, a.splits, stream, up_args);
   if (e != cudaSuccess) return e;
   // The widest cluster with which every CTA resides at once, and several to a tile where there are few tiles.  With
-  // two CTAs on an SM clusters of 4: those of 8 (and 16) do not all find room in the GPU's SM groups, and one cluster
-  // that has to wait costs a second wave (45 us at 64 tokens).
-  const int row_tiles = (a.H + kUnitRows - 1) / kUnitRows, room = kFew ? dev->sms : resident;
-  a.splits = kFew ? 8 : 4;
-  while (a.splits > 1 && row_tiles * a.splits > room) a.splits /= 2;
-  a.parts = row_tiles <= kMaxSharedTiles ? room / (row_tiles * a.splits) : 1;
+  // two CTAs on an SM clusters of at most 4: of 8 (and 16) fewer fit, and one that has to wait costs a second wave
+  // (45 us at 64 tokens).
+  const int row_tiles = (a.H + kUnitRows - 1) / kUnitRows, down_smem = D::bytes(kFew ? G : kMoeMaxTokens);
+  const int room = kFew ? dev->sms : resident;
+  static Resident known;
+  int fit = 0;
+  for (a.splits = kFew ? 8 : 4; a.splits > 1; a.splits /= 2) {
+    fit = (G == kSmallGroup ? 2 : 1) * resident_clusters(down, kMoeThreads, down_smem, a.splits, known);
+    if (fit > room / a.splits) fit = room / a.splits;
+    if (fit >= row_tiles) break;
+  }
+  if (a.splits == 1) fit = room;
+  a.parts = row_tiles <= kMaxSharedTiles ? fit / row_tiles : 1;
   a.parts = a.parts < 1 ? 1 : (a.parts > kMaxParts ? kMaxParts : a.parts);
   void* down_args[] = {&m2, &a};
   return launch_pdl(down, dim3((unsigned)(row_tiles * a.splits * a.parts)), dim3(kMoeThreads), D::bytes(a.T), a.splits,
