@@ -189,6 +189,53 @@ def test_prep_keeps_non_finite_values_to_their_block_or_row(K):
     assert np.array_equal(row[[0, 3]], values(check.codes)[[0, 3]])
 
 
+# Rows enough that each thread holds four vectors of one: up to 8192 columns, up to 20480, and beyond
+MANY = [(200, 1040), (161, 3584), (300, 4112), (150, 8192), (149, 8208), (5, 20480), (3, 24000)]
+
+
+@pytest.mark.parametrize("T,K", MANY)
+def test_prep_of_many_rows(T, K):
+    x = synthetic.activations(80 + K, T, K)
+    r = synthetic.activations(81 + K, T, K)
+    x[0, :K // 2] = 0.0
+    gamma = synthetic.gamma(82, K)
+    X, _ = strided(x, 8)
+    R, _ = strided(r, 16)
+    act, codes, scales = make_act(T, K, lds_pad=4)
+    act.prep(X)
+    q, s = O.quant(x)
+    assert np.array_equal(act.scales.cpu().numpy(), s) and np.array_equal(values(act.codes), q)
+    act.prep(X, H.bf16_dev(gamma), EPS)
+    check_quant(act, O.rms_norm(x, gamma, np.float32(EPS)), norm_delta(K))
+    h = (torch.from_numpy(x) + torch.from_numpy(r)).bfloat16().float().numpy()
+    act.prep_residual(X, R, R, H.bf16_dev(gamma), EPS)
+    check_quant(act, O.rms_norm(h, gamma, np.float32(EPS)), norm_delta(K))
+    assert np.array_equal(R.float().cpu().numpy(), h)
+    act.prep_silu_mul(X, R)
+    check_quant(act, O.silu(x) * h, (2 + 1.2 * 88 + 8) * 2.0 ** -23)
+    check_untouched(act, codes, scales)
+
+
+@pytest.mark.parametrize("K", [512, 1040, 4096, 9000 // 16 * 16])
+def test_prep_norm_of_blocks_far_below_their_row(K):
+    """a row of small root mean square with a block so small that its scale is the smallest normal number: the factor
+    gamma / rms / scale leaves float32 although the codes are ordinary"""
+    x = np.full((3, K), 2.0 ** -20, np.float32)
+    x[:, :128] = 2.0 ** -133 * np.arange(1, 129)  # bf16 values, some subnormal
+    x[1, :128] = 0.0
+    x = torch.from_numpy(x).bfloat16().float().numpy()
+    gamma = np.ones(K, np.float32)
+    act, _, _ = make_act(3, K)
+    act.prep(H.bf16_dev(x), H.bf16_dev(gamma), 0.0)
+    v = O.rms_norm(x, gamma, 0.0)
+    s = f64(act.scales)
+    assert s[1, 0] == 1.0 and (s > 0).all()
+    # below 2^-126 a float32 product is off by up to half its spacing 2^-149, which is 2^-24 of the smallest scale
+    err = np.abs(values(act.codes) * O.expand(s, K, 1) - v)
+    se = O.expand(s, K, 1)
+    assert (err <= np.abs(v) * (2.0 ** -4 + norm_delta(K) + 2.0 ** -22) + se * (2.0 ** -10 * (1 + 2.0 ** -20) + 2.0 ** -23)).all()
+
+
 def test_prep_without_rows():
     act = sq.Fp8Act(0, 256)
     e = torch.empty(0, 256, dtype=torch.bfloat16, device="cuda")
@@ -198,7 +245,8 @@ def test_prep_without_rows():
     torch.cuda.synchronize()
 
 
-@pytest.mark.parametrize("E,K,D", [(1, 16, 1), (1, 128, 128), (1, 272, 129), (3, 2000, 1100), (2, 144, 264), (1, 4096, 512)])
+@pytest.mark.parametrize("E,K,D", [(1, 16, 1), (1, 128, 128), (1, 272, 129), (3, 2000, 1100), (2, 144, 264), (1, 4096, 512), (2, 300 // 16 * 16, 130),
+                                   (1, 160, 77)])
 def test_pack_is_bit_exact(E, K, D):
     W = synthetic.weights(70 + E, E * K, D).reshape(E, K, D).copy()
     W[0, :128, :128] = 0.0
@@ -249,7 +297,7 @@ def check_linear(y, ref, bound, dtype):
 
 
 LINEAR = [(1, 16, 1), (1, 3584, 512), (2, 144, 15), (7, 1024, 17), (8, 4112, 129), (9, 272, 264), (16, 18944, 96),
-          (17, 128, 128), (17, 16, 1), (33, 4112, 250), (64, 3584, 640), (127, 1040, 129), (128, 128, 127),
+          (17, 128, 128), (17, 16, 1), (32, 1040, 640), (33, 4112, 250), (65, 400, 130), (3, 272, 38100), (64, 3584, 640), (127, 1040, 129), (128, 128, 127),
           (129, 272, 1111), (200, 4096, 257), (333, 2064, 300), (700, 144, 2000)]
 
 
@@ -270,7 +318,7 @@ def test_linear(T, K, D, dtype):
 # enough 256 x 256 tiles for the pair kernel: whole tiles, and both axes (and the second CTA's half) ragged
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("T,K,D", [(2048, 512, 2560), (2100, 400, 2500), (2180, 144, 2705), (260, 272, 19000),
-                                   (19000, 272, 260)])
+                                   (19000, 272, 260), (2049, 1040, 2560), (4000, 640, 5000)])
 def test_linear_pair(T, K, D, dtype):
     x, xs, w, ws = operands(T, K, D, T + K + D)
     act = sq.Fp8Act.from_parts(x.cuda(), xs.cuda())
@@ -364,7 +412,8 @@ def check_moe(out, x, lg, w13, s13, w2, s2, topk, renormalize=True):
 
 
 MOE = [(1, 1, 1, 16, 16), (1, 4, 2, 128, 64), (1, 128, 8, 256, 96), (2, 8, 2, 272, 144), (7, 16, 4, 2064, 48),
-       (16, 8, 2, 256, 768), (33, 60, 6, 144, 272), (64, 8, 8, 256, 128), (64, 512, 16, 128, 32), (64, 128, 8, 512, 96)]
+       (16, 8, 2, 256, 768), (33, 60, 6, 144, 272), (64, 8, 8, 256, 128), (64, 512, 16, 128, 32), (64, 128, 8, 512, 96), (1, 1, 1, 2064, 64), (2, 300, 3, 1040, 16),
+       (8, 9, 9, 128, 80), (9, 40, 4, 640, 128), (24, 3, 2, 272, 128), (40, 4, 2, 1040, 272)]
 
 
 @pytest.mark.parametrize("T,E,topk,Hd,I", MOE)
@@ -402,9 +451,97 @@ def test_moe_all_tokens_on_the_same_experts():
     check_moe(run_moe(x, lg, *w, 2), x, lg, *w, 2)
 
 
+@pytest.mark.parametrize("T", [4, 20, 60])
+def test_moe_padded_rows_may_hold_anything(T):
+    """tokens whose logits are all -inf take no part: y = 0 whatever their x, and nobody else's result changes"""
+    x, lg, *w = moe_inputs(T, 12, 272, 144, 11)
+    pad = torch.arange(T) % 3 == 2
+    lg[pad] = float("-inf")
+    x = x.clone()
+    x[pad] = float("nan")
+    y, ids, p = run_moe(x, lg, *w, 3)
+    assert (y[pad] == 0).all() and (p[pad] == 0).all()
+    keep = ~pad
+    check_moe((y[keep], ids[keep], p[keep]), x[keep], lg[keep], *w, 3)
+    assert np.array_equal(ids[pad].cpu().numpy(), O.route(f64(lg[pad]), 3)[0])
+
+
+@pytest.mark.parametrize("T", [5, 20, 64])
+def test_moe_nan_and_inf_stay_with_their_token(T):
+    x, lg, *w = moe_inputs(T, 10, 272, 144, 12)
+    x = x.clone()
+    x[1, 3], x[2, 200] = float("nan"), float("inf")
+    y, _, _ = run_moe(x, lg, *w, 2)
+    bad = torch.zeros(T, dtype=torch.bool)
+    bad[1] = bad[2] = True
+    assert y[1].isnan().all()
+    assert not y[2].isfinite().any()
+    ref, _, _ = run_moe(torch.where(bad[:, None], torch.zeros_like(x), x), lg, *w, 2)
+    assert torch.equal(y[~bad], ref[~bad])
+
+
+def test_moe_one_workspace_for_calls_of_every_size():
+    """the arrival counts that calls leave behind are zero again, whatever the sizes"""
+    args = {T: moe_inputs(T, 16, 640, 128, T) for T in (1, 8, 9, 30, 64)}
+    a = {T: (sq.Fp8Weight.from_parts(v[2].cuda(), v[3].cuda()), sq.Fp8Weight.from_parts(v[4].cuda(), v[5].cuda()))
+         for T, v in args.items()}
+    ws = sq.Fp8Workspace.for_moe(64, 4, *a[64])
+    for T in (64, 1, 30, 8, 9, 64, 30, 1):
+        x, lg = args[T][:2]
+        out = sq.fp8_moe(x.cuda(), lg.cuda(), *a[T], 4, ws=ws, return_routing=True)
+        check_moe(out, *args[T], 4)
+        again = sq.fp8_moe(x.cuda(), lg.cuda(), *a[T], 4, ws=ws)
+        assert torch.equal(out[0], again)  # the same bits again
+    assert ws.check() == 0
+
+
+def test_weights_beyond_two_gigabytes():
+    """offsets that pass 32 bits: the last experts of a large layer, the last columns of a large linear"""
+    E, Hd, I = 140, 4096, 2048
+    g = torch.Generator(device="cuda").manual_seed(5)
+    bytes_ = torch.randint(0, 256, (2 * I * Hd + 1,), generator=g, device="cuda", dtype=torch.uint8)
+    bytes_ = torch.where(bytes_ & 0x7F >= 0x70, bytes_ & 0x8F, bytes_)  # no NaN, nothing above 15
+    one13, one2 = bytes_[:-1].view(2 * I, Hd), bytes_[1:1 + Hd * I].view(Hd, I)
+    w13, w2 = (torch.zeros(E, *t.shape, dtype=torch.uint8, device="cuda") for t in (one13, one2))
+    for e in (0, 130, 139):
+        w13[e], w2[e] = one13.roll(e, 0), one2.roll(e, 0)
+    s13 = torch.full((E, 2 * I // 128, Hd // 128), 2.0 ** -9, device="cuda")
+    s2 = torch.full((E, Hd // 128, I // 128), 2.0 ** -9, device="cuda")
+    x = torch.randn(2, Hd, generator=g, device="cuda").bfloat16()
+    lg = torch.full((2, E), -9.0, device="cuda")
+    lg[0, 139], lg[0, 0], lg[1, 130], lg[1, 139] = 3.0, 2.0, 1.0, 0.5
+    y, ids, p = sq.fp8_moe(x, lg, sq.Fp8Weight.from_parts(w13.view(F8), s13), sq.Fp8Weight.from_parts(w2.view(F8), s2),
+                           2, return_routing=True)
+    assert ids.tolist() == [[139, 0], [130, 139]]
+    for t in range(2):
+        ref, size = 0.0, 0.0
+        for j in range(2):
+            a13, a2 = (w[int(ids[t, j])].view(F8).double() * 2.0 ** -9 for w in (w13, w2))
+            gu = a13 @ x[t].double()
+            h = gu[:I] * torch.sigmoid(gu[:I]) * gu[I:]
+            ref = ref + float(p[t, j]) * (a2 @ h)
+            size = size + float(p[t, j]) * (a2.abs() @ h.abs())
+        # h off by 2^-12 of itself as three terms and less by its own sums; sums of I terms; bf16
+        assert ((y[t].double() - ref).abs() <= 2.0 ** -8 * ref.abs() + (2.0 ** -11 + 2 * I * 2.0 ** -23) * size).all()
+    del w13, w2
+    K, D = 16384, 140000
+    code = torch.empty(D, K, dtype=torch.uint8, device="cuda")
+    for d in range(0, D, 2 * I):
+        n = min(2 * I, D - d)
+        code[d:d + n] = bytes_[:n * Hd].view(n, Hd).repeat(1, K // Hd).roll(d // 7, 0)
+    scale = torch.full((O.blocks(D), K // 128), 2.0 ** -9, device="cuda")
+    act = sq.Fp8Act(3, K).prep(torch.randn(3, K, generator=g, device="cuda").bfloat16())
+    y = sq.fp8_linear(act, sq.Fp8Weight.from_parts(code.view(F8), scale), out_dtype=torch.float32)
+    xd = act.codes.double() * act.scales.double().repeat_interleave(128, 1)
+    for d in (0, 131000, D - 300):
+        wd = code[d:d + 300].view(F8).double() * 2.0 ** -9
+        ref, size = xd @ wd.T, xd.abs() @ wd.abs().T
+        assert ((y[:, d:d + 300].double() - ref).abs() <= (128 + K // 128 + 8) * 2.0 ** -23 * size + 2.0 ** -24 * ref.abs()).all()
+
+
 @pytest.mark.parametrize("mag", [2.0 ** -110, 2.0 ** -40, 2.0 ** 40])
 def test_moe_activations_far_from_one(mag):
-    """f16 operands hold any bf16 activation: its 128-block is scaled by a power of two"""
+    """E4M3 terms hold any bf16 activation: its 128-block is scaled by a power of two"""
     x, lg, w13, s13, w2, s2 = moe_inputs(5, 4, 256, 128, 8)
     x = (x.float() * mag).bfloat16()
     x[3, :128] = 0
