@@ -377,7 +377,8 @@ int sharq_linear_grouped(const sharq_act *a, const int *d_group_offsets, const s
  * Non-finite inputs: a NaN stays a NaN of its own; an infinity makes its
  * 128-block NaN.  They reach the outputs that depend on them and no others.
  * All kernels are launched as programmatic dependents and read nothing before
- * the preceding kernel of the stream has completed.
+ * the preceding kernel of the stream has completed (a linear may bring weights
+ * into L2 earlier).
  * ---------------------------------------------------------------------------
  */
 
@@ -390,8 +391,9 @@ typedef struct {
 } sharq_fp8_weight;
 
 /* codes: E4M3 [T][K]; scales: float32 [ceil(K/128)][lds], the scale of row t
- * and block b at b * lds + t (lds >= T, a multiple of 4; entries past T are
- * neither read nor written). */
+ * and block b at b * lds + t (lds >= T, a multiple of 4; entries past T are not
+ * used and never written, but lie within the buffer: up to three are read with
+ * the ones before). */
 typedef struct {
   void *codes;
   float *scales;
@@ -462,7 +464,8 @@ int sharq_fp8_linear(const sharq_fp8_act *a, const sharq_fp8_weight *w, void *d_
 
 /*
  * sharq_fp8_moe - a whole mixture-of-experts layer for a few tokens (decode),
- * in two kernels.  Larger batches belong to a grouped GEMM.
+ * in two kernels up to 8 tokens and three above (one that chooses the experts).
+ * Larger batches belong to a grouped GEMM.
  *   chosen(t): the topk largest of d_logits[t][0..E-1] (float32, row stride
  *     ldl), equal logits by the lower index.
  *   p(t, j): softmax over the chosen logits (renormalize != 0) or the chosen
@@ -475,12 +478,13 @@ int sharq_fp8_linear(const sharq_fp8_act *a, const sharq_fp8_weight *w, void *d_
  * are not quantized: x enters as two E4M3 terms of a power-of-two scale per 128
  * (exact down to 2^-13 of the block's largest), h (float32) as three (2^-12
  * relative).  An expert of weight 0 is not evaluated, so a masked token's x may
- * hold anything.  d_Y: bf16 [T][H], row stride ldy; it may be d_X.  d_topk_ids (int32) and d_topk_weights (float32), [T][topk]: written
- * unless NULL.
+ * hold anything.  d_Y: bf16 [T][H], row stride ldy; it may be d_X.  d_topk_ids
+ * (int32) and d_topk_weights (float32), [T][topk]: written unless NULL.
  * T <= 64, topk <= 16 and <= E, E <= 512 (SHARQ_ERR_UNSUPPORTED_SHAPE).
  * d_ws: at least sharq_fp8_moe_workspace_bytes, zeroed once before its first use
- * (its first word is the error word of sharq_check_status); calls that may run
- * at the same time need one each.
+ * (its first word is the error word of sharq_check_status, and counts that every
+ * call leaves at zero follow); calls that may run at the same time need one each.
+ * One workspace serves calls of every size that it is large enough for.
  */
 #define SHARQ_FP8_MOE_MAX_T 64
 #define SHARQ_FP8_MOE_MAX_TOPK 16
