@@ -554,15 +554,24 @@ __global__ void __launch_bounds__(Pair::kThreads, 1)
   // the smaller operand is walked fastest, so that it stays in L2 while the
   // larger one streams past it once
   const bool m_fast = a.T <= a.D;
-  auto coords = [&](int tile, int& mt, int& nt) {
-    if (m_fast) {
-      nt = tile / m_tiles;
-      mt = tile - nt * m_tiles;
-    } else {
-      mt = tile / n_tiles;
-      nt = tile - mt * n_tiles;
+  const int inner = m_fast ? m_tiles : n_tiles;
+  // a role's walk over this pair's tiles; the division is done once
+  struct Walk {
+    int tile, in, out;
+  };
+  const int step_out = npairs / inner, step_in = npairs - step_out * inner;
+  auto first_tile = [&]() { return Walk{pair, pair % inner, pair / inner}; };
+  auto next_tile = [&](Walk& w) {
+    w.tile += npairs;
+    w.in += step_in;
+    w.out += step_out;
+    if (w.in >= inner) {
+      w.in -= inner;
+      ++w.out;
     }
   };
+  auto row_tile = [&](const Walk& w) { return m_fast ? w.in : w.out; };
+  auto col_tile = [&](const Walk& w) { return m_fast ? w.out : w.in; };
 
   if (threadIdx.x == 0) {
     tma_prefetch_map(&mapx);
@@ -596,9 +605,8 @@ __global__ void __launch_bounds__(Pair::kThreads, 1)
       const uint32_t full_lead = mapa_shared(smem_u32(&full_bar[0]), 0);
       int i = 0, s = 0;
       uint32_t phase = 1;  // of the slot's previous use
-      for (int tile = pair; tile < ntiles && !abort_sh; tile += npairs) {
-        int mt, nt;
-        coords(tile, mt, nt);
+      for (Walk w = first_tile(); w.tile < ntiles && !abort_sh; next_tile(w)) {
+        const int mt = row_tile(w), nt = col_tile(w);
         const uint64_t deadline = globaltimer_ns() + kWaitNs;
         for (int b = 0; b < nkb; ++b, ++i) {
           if (i >= C::kStages && !mbar_wait(&empty_bar[s], phase, deadline, &abort_sh)) {
@@ -684,19 +692,17 @@ __global__ void __launch_bounds__(Pair::kThreads, 1)
         nw[j] = ws[b];
       }
     };
-    auto scales = [&](int tile) {
-      int mt, nt;
-      coords(tile, mt, nt);
+    auto scales = [&](const Walk& w) {
+      const int mt = row_tile(w), nt = col_tile(w);
       xs = a.xs + min(mt * C::BM + (int)rank * 128 + sp * 32 + lane, a.T - 1);
       ws = a.ws + (size_t)min(nt * 2 + half, d_blocks - 1) * nkb;
       load_scales(0);
     };
     bool seen = false;  // the next buffer was full when it was asked for
-    if (pair < ntiles) scales(pair);
-    for (int tile = pair; tile < ntiles && !abort_sh; tile += npairs) {
-      int mt, nt;
-      coords(tile, mt, nt);
-      const int row0 = mt * C::BM + (int)rank * 128 + sp * 32;
+    Walk w = first_tile();
+    if (w.tile < ntiles) scales(w);
+    while (w.tile < ntiles) {
+      const int row0 = row_tile(w) * C::BM + (int)rank * 128 + sp * 32, col0 = col_tile(w) * C::BN + half * 128;
       float acc[128] = {};
       for (int b0 = 0; b0 < nkb; b0 += kGroup) {
         float s[kGroup];
@@ -731,8 +737,8 @@ __global__ void __launch_bounds__(Pair::kThreads, 1)
           }
         }
       }
-      if (tile + npairs < ntiles) scales(tile + npairs);  // on their way while this tile is stored
-      const int col0 = nt * C::BN + half * 128;
+      next_tile(w);
+      if (w.tile < ntiles) scales(w);  // on their way while this tile is stored
       if (row0 < a.T && col0 < a.D && !abort_sh) {
         uint32_t o[32];
         if (lane == 0) bulk_wait_read_all();  // the last tile's stores have left the staging area
