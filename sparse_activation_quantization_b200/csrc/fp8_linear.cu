@@ -262,6 +262,35 @@ cudaError_t launch_skinny(LinearArgs& a, const Device* dev, cudaStream_t stream)
                     args);
 }
 
+// Scales of a row's next four blocks, on their way while four are added:
+// everything that goes through the load path is slow beside the MMAs' operand
+// reads, and a load (and a shuffle) per block took 300 cycles of it.
+struct ScaleGroup {
+  static constexpr int kBlocks = 4;
+  const float *xs, *ws;  // the row's column of X's scales, the tile's row of W's
+  int lds, end;
+  float nx[kBlocks], nw[kBlocks];
+  __device__ __forceinline__ void load(int b0) {
+#pragma unroll
+    for (int j = 0; j < kBlocks; ++j) {
+      const int b = min(b0 + j, end - 1);
+      nx[j] = xs[(size_t)b * lds];
+      nw[j] = ws[b];
+    }
+  }
+  // blocks b0 .. b1 - 1, at least one
+  __device__ __forceinline__ void start(const float* x, int ld, const float* w, int b0, int b1) {
+    xs = x, ws = w, lds = ld, end = b1;
+    load(b0);
+  }
+  // the products of blocks b .. b + 3; the next four are asked for
+  __device__ __forceinline__ void take(float (&s)[kBlocks], int b) {
+#pragma unroll
+    for (int j = 0; j < kBlocks; ++j) s[j] = nx[j] * nw[j];
+    if (b + kBlocks < end) load(b + kBlocks);
+  }
+};
+
 // -------------------------------------------------------------- tile form ---
 // 128 x 128 output tile per CTA (or per cluster of S CTAs that share its K).
 //   warp 0      producer: per 128-k block one box of X and one of W (16 KB
@@ -380,31 +409,38 @@ __global__ void __launch_bounds__(Tile::kThreads, 1)
     const int sp = warp & 3, half = (warp - 4) >> 2;  // TMEM lane quarter; column half
     const int rl = sp * 32 + lane, row = mt * C::BM + rl;
     const uint32_t col0 = (uint32_t)half * 64;
-    const float* xs = a.xs + min(row, a.T - 1);
-    const float* ws = a.ws + (size_t)nt * nkb;
+    ScaleGroup sg;
+    sg.start(a.xs + min(row, a.T - 1), a.lds, a.ws + (size_t)nt * nkb, b0, b1);
     float acc[64] = {};
-    float s_next = b0 < b1 ? xs[(size_t)b0 * a.lds] * ws[b0] : 0.0f;
-    for (int b = b0, i = 0; b < b1; ++b, ++i) {
-      const int u = i % C::kBufs;
-      const float s = s_next;
-      if (b + 1 < b1) s_next = xs[(size_t)(b + 1) * a.lds] * ws[b + 1];
-      if (!__all_sync(0xffffffffu, mbar_wait(&acc_full[u], (i / C::kBufs) & 1, deadline, &abort_sh))) {
-        record_error_word(a.err, kErrTimeoutWord);
-        abort_sh = 1;
-        break;
-      }
-      tc_fence_after();
-      uint32_t v[2][32];
-      const uint32_t src = tmem + ((uint32_t)(sp * 32) << 16) + u * C::BN + col0;
-      tmem_ld32(src, v[0]);
-      tmem_ld32(src + 32, v[1]);
-      tmem_ld_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_cta(&acc_empty[u]);
+    bool seen = false;  // the next buffer was full when it was asked for
+    int i = 0;
+    for (int g0 = b0; g0 < b1; g0 += ScaleGroup::kBlocks) {
+      float s[ScaleGroup::kBlocks];
+      sg.take(s, g0);
 #pragma unroll
-      for (int c = 0; c < 64; c += 2)
-        fma2(acc[c], acc[c + 1], __uint_as_float(v[c >> 5][c & 31]), __uint_as_float(v[c >> 5][(c & 31) + 1]), s);
+      for (int j = 0; j < ScaleGroup::kBlocks; ++j) {
+        if (g0 + j >= b1) break;
+        const int u = i % C::kBufs;
+        // where a wait runs out the warp goes on as one, with sums that nobody stores
+        if (!seen && !mbar_wait_short(&acc_full[u], (i / C::kBufs) & 1, &abort_sh)) {
+          record_error_word(a.err, kErrTimeoutWord);
+          abort_sh = 1;
+        }
+        ++i;
+        __syncwarp();
+        tc_fence_after();
+        uint32_t v[64];
+        const uint32_t src = tmem + ((uint32_t)(sp * 32) << 16) + u * C::BN + col0;
+        tmem_read(src, v);
+        tmem_ld_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cta(&acc_empty[u]);
+        seen = mbar_test(&acc_full[i % C::kBufs], (i / C::kBufs) & 1);  // answered while these are added
+#pragma unroll
+        for (int c = 0; c < 64; c += 2)
+          fma2(acc[c], acc[c + 1], __uint_as_float(v[c]), __uint_as_float(v[c + 1]), s[j]);
+      }
     }
     // the last block's sums were read, so every MMA has completed and with it
     // every use of the ring
@@ -678,25 +714,11 @@ __global__ void __launch_bounds__(Pair::kThreads, 1)
     const int d_blocks = blocks_of(a.D);
     const uint32_t src = tmem + ((uint32_t)(sp * 32) << 16) + half * 64;
     int n = 0;  // buffers taken
-    // Scales of the next four blocks, on their way while four are added: everything
-    // that goes through the load path is slow beside the MMAs' operand reads, and
-    // a load and a shuffle per block took 300 cycles of it.
-    constexpr int kGroup = 4;
-    const float *xs = nullptr, *ws = nullptr;
-    float nx[kGroup], nw[kGroup];
-    auto load_scales = [&](int b0) {
-#pragma unroll
-      for (int j = 0; j < kGroup; ++j) {
-        const int b = min(b0 + j, nkb - 1);
-        nx[j] = xs[(size_t)b * a.lds];
-        nw[j] = ws[b];
-      }
-    };
+    ScaleGroup sg;
     auto scales = [&](const Walk& w) {
       const int mt = row_tile(w), nt = col_tile(w);
-      xs = a.xs + min(mt * C::BM + (int)rank * 128 + sp * 32 + lane, a.T - 1);
-      ws = a.ws + (size_t)min(nt * 2 + half, d_blocks - 1) * nkb;
-      load_scales(0);
+      sg.start(a.xs + min(mt * C::BM + (int)rank * 128 + sp * 32 + lane, a.T - 1), a.lds,
+               a.ws + (size_t)min(nt * 2 + half, d_blocks - 1) * nkb, 0, nkb);
     };
     bool seen = false;  // the next buffer was full when it was asked for
     Walk w = first_tile();
@@ -704,13 +726,11 @@ __global__ void __launch_bounds__(Pair::kThreads, 1)
     while (w.tile < ntiles) {
       const int row0 = row_tile(w) * C::BM + (int)rank * 128 + sp * 32, col0 = col_tile(w) * C::BN + half * 128;
       float acc[128] = {};
-      for (int b0 = 0; b0 < nkb; b0 += kGroup) {
-        float s[kGroup];
+      for (int b0 = 0; b0 < nkb; b0 += ScaleGroup::kBlocks) {
+        float s[ScaleGroup::kBlocks];
+        sg.take(s, b0);
 #pragma unroll
-        for (int j = 0; j < kGroup; ++j) s[j] = nx[j] * nw[j];
-        if (b0 + kGroup < nkb) load_scales(b0 + kGroup);
-#pragma unroll
-        for (int j = 0; j < kGroup; ++j) {
+        for (int j = 0; j < ScaleGroup::kBlocks; ++j) {
           if (b0 + j >= nkb) break;
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
