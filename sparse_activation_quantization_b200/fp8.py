@@ -107,8 +107,6 @@ class Fp8Weight:
         if W.dim() not in (2, 3):
             raise ValueError("W must be [K, D] or [E, K, D]")
         E, K, D = (1, *W.shape) if W.dim() == 2 else W.shape
-        if _sq.sharq_fp8_weight_bytes(K, D, E) == 0:
-            raise _sq.SharqError(-2, "sharq_fp8_weight_bytes")
         lead = () if W.dim() == 2 else (E,)
         if _elsewhere(W.device, stream):
             with _on(W.device, stream):
