@@ -125,7 +125,7 @@ __global__ void __launch_bounds__(Skinny<kN>::kThreads, 2)
   if (threadIdx.x == 128) {
     tma_prefetch_map(&mapx);
     tma_prefetch_map(&mapw);
-    bars.init(1);
+    bars.init(1, 1);
     for (int i = 0; i < C::kStages && b0 + i < b1; ++i)
       tma_prefetch_2d(&mapw, (b0 + i) * kBlock, first * kUnitRows);
   }
@@ -165,15 +165,19 @@ __global__ void __launch_bounds__(Skinny<kN>::kThreads, 2)
   } else if (warp == 5) {
     if (elect_one()) {
       RingPos<C::kStages> p;
+      bool ready = false;  // the next unit had landed when it was asked for, before the MMAs ahead of it
       for (int tile = first; tile < tiles && !bars.abort; tile += step)
-        for (int b = b0; b < b1; ++b, p.next()) {
-          if (!mbar_wait(&bars.full[p.s], p.phase, deadline, &bars.abort)) {
+        for (int b = b0; b < b1; ++b) {
+          if (!ready && !mbar_wait(&bars.full[p.s], p.phase, deadline, &bars.abort)) {
             bars.give_up(a.err);
             break;
           }
+          const int s = p.s;
+          p.next();
+          ready = mbar_test(&bars.full[p.s], p.phase);
           tc_fence_after();
-          unit_mma(tmem + p.s * kN, smem_u32(smem + p.s * C::kStageBytes), idesc_e4m3(kUnitRows, kN));
-          tc_commit(&bars.done[p.s]);
+          unit_mma(tmem + s * kN, smem_u32(smem + s * C::kStageBytes), idesc_e4m3(kUnitRows, kN));
+          tc_commit(&bars.done[s]);
         }
     }
   } else {

@@ -416,31 +416,82 @@ __device__ __forceinline__ bool form_columns(uint8_t* dst, float* scale, int np,
 
 __host__ __device__ constexpr int mma_n(int cols) { return (cols + 15) / 16 * 16; }
 
-// One finished unit's sums: acc[t] += (c1 + c2 / 16 (+ c3 / 256)) scale[t] s_w
+// One unit's MMAs, by the issuing thread, which has seen the stage's columns and
+// scales arrive and therefore arrives on done itself as well: who waits for done
+// then sees the scales too, and the sum warps need not wait on full.  `ready`:
+// whether this unit was full when it was asked for; on return, whether the next
+// one is.  (A question asked behind MMAs is answered when they are taken in, 200
+// cycles later: it is asked before them.)
+template <int kStages>
+__device__ __forceinline__ bool issue_unit(SkinnyBars<kStages>& bars, RingPos<kStages>& p, bool& ready, uint32_t tmem,
+                                           int stage_cols, const uint8_t* ring, int stage_bytes, uint32_t idesc,
+                                           uint64_t deadline) {
+  if (!ready && !mbar_wait(&bars.full[p.s], p.phase, deadline, &bars.abort)) return false;
+  const int s = p.s;
+  p.next();
+  ready = mbar_test(&bars.full[p.s], p.phase);
+  tc_fence_after();
+  unit_mma(tmem + s * stage_cols, smem_u32(ring + s * stage_bytes), idesc);
+  tc_commit(&bars.done[s]);
+  mbar_arrive_cta(&bars.done[s]);
+  return true;
+}
+
+// One unit's sums: acc[t] += (c1 + c2 / 16 (+ c3 / 256)) scale[t] s_w.  `seen`: the
+// unit was done when it was asked for; on return, whether the next one is.  Where
+// a wait runs out the flag is set and the warp goes on as one, with sums that
+// nobody stores.
 template <int J, int P, int kStages>
-__device__ __forceinline__ bool add_unit(SkinnyBars<kStages>& bars, RingPos<kStages>& pos, uint32_t tmem_lane,
-                                         int stage_cols, const float* scale, float s_w, float (&acc)[P],
-                                         uint64_t deadline, int lane) {
-  if (!wait_done(bars, pos, deadline)) return false;
-  uint32_t v[J * P];
-  tmem_read(tmem_lane + pos.s * stage_cols, v);
-  tmem_ld_wait();
+__device__ __forceinline__ void add_unit(SkinnyBars<kStages>& bars, RingPos<kStages>& pos, bool& seen,
+                                         uint32_t tmem_lane, int stage_cols, const float* scale, float s_w,
+                                         float (&acc)[P], int* err, int lane) {
+  if (!seen && !mbar_wait_short(&bars.done[pos.s], pos.phase, &bars.abort)) bars.give_up(err);
+  __syncwarp();
+  tc_fence_after();
+  float s[P];
 #pragma unroll
   for (int t = 0; t < P; t += 4) {
     const float4 s4 = *reinterpret_cast<const float4*>(scale + t);
-    const float s[4] = {s4.x, s4.y, s4.z, s4.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      float c = __uint_as_float(v[(J - 1) * P + t + i]);
-#pragma unroll
-      for (int j = J - 2; j >= 0; --j) c = fmaf(c, 0.0625f, __uint_as_float(v[j * P + t + i]));
-      acc[t + i] = fmaf(c, s[i] * s_w, acc[t + i]);
-    }
+    s[t] = s4.x, s[t + 1] = s4.y, s[t + 2] = s4.z, s[t + 3] = s4.w;
   }
+  uint32_t v[J * P];
+  tmem_read(tmem_lane + pos.s * stage_cols, v);
+  tmem_ld_wait();
   release_unit(bars, pos, lane);
   pos.next();
-  return true;
+  seen = mbar_test(&bars.done[pos.s], pos.phase);  // answered while this unit is added
+#pragma unroll
+  for (int t = 0; t < P; ++t) {
+    float c = __uint_as_float(v[(J - 1) * P + t]);
+#pragma unroll
+    for (int j = J - 2; j >= 0; --j) c = fmaf(c, 0.0625f, __uint_as_float(v[j * P + t]));
+    acc[t] = fmaf(c, s[t] * s_w, acc[t]);
+  }
 }
+
+// The weight scales of a unit whose 32 rows a warp are 16 gate rows and 16 up rows:
+// each half of the warp holds its row's scales, 16 blocks at a time.
+struct HalfScales {
+  const float* p;
+  int n, base;
+  float cur, ahead;
+  __device__ __forceinline__ float load(int b) const { return b < n ? p[b] : 0.0f; }
+  __device__ __forceinline__ void start(const float* row, int blocks, int b0, int lane) {
+    p = row;
+    n = blocks;
+    base = b0;
+    cur = load(b0 + (lane & 15));
+    ahead = load(b0 + 16 + (lane & 15));
+  }
+  __device__ __forceinline__ float at(int b, int lane) {  // b ascends
+    if (b - base >= 16) {
+      base += 16;
+      cur = ahead;
+      ahead = load(base + 16 + (lane & 15));
+    }
+    return __shfl_sync(0xffffffffu, cur, (lane & 16) | (b - base));
+  }
+};
 
 template <int J, int G, int Stages>
 struct MoeRing {
@@ -472,7 +523,7 @@ template <class R>
 __device__ __forceinline__ void moe_setup(SkinnyBars<R::kStages>& bars, const CUtensorMap* map) {
   if (threadIdx.x == kSumWarps * 32) {
     tma_prefetch_map(map);
-    bars.init(2);
+    bars.init(2, 2);  // full: the copy and the forming warp; done: the MMAs and the thread that issued them
   }
   if (threadIdx.x >> 5 == kSumWarps + 1) {
     tmem_alloc(&bars.tmem, R::kTmem);
@@ -546,17 +597,14 @@ __global__ void __launch_bounds__(kMoeThreads, G == kSmallGroup ? 2 : 1)
   } else if (warp == kSumWarps + 1) {
     if (elect_one()) {
       Pos p;
+      bool ready = false;
       for (int it = it0; it < it1 && !bars.abort; ++it) {
         const uint32_t idesc = idesc_e4m3(kUnitRows, mma_n(kUpTerms * r.groups[it / tiles].form));
-        for (int b = b0; b < b1; ++b, p.next()) {
-          if (!mbar_wait(&bars.full[p.s], p.phase, deadline, &bars.abort)) {
+        for (int b = b0; b < b1; ++b)
+          if (!issue_unit(bars, p, ready, tmem, C::kCols, smem, C::kStageBytes, idesc, deadline)) {
             bars.give_up(a.err);
             break;
           }
-          tc_fence_after();
-          unit_mma(tmem + p.s * C::kCols, smem_u32(smem + p.s * C::kStageBytes), idesc);
-          tc_commit(&bars.done[p.s]);
-        }
       }
     }
   } else if (warp >= kFirstFormWarp) {
@@ -582,6 +630,7 @@ __global__ void __launch_bounds__(kMoeThreads, G == kSmallGroup ? 2 : 1)
     }
   } else {
     Pos p;
+    bool seen = false;
     const int rb = blocks_of(2 * a.I);
     const uint32_t tmem_lane = tmem + ((uint32_t)(warp * 32) << 16);
     for (int it = it0; it < it1 && !bars.abort; ++it) {
@@ -590,19 +639,14 @@ __global__ void __launch_bounds__(kMoeThreads, G == kSmallGroup ? 2 : 1)
       // the warp's 16 gate rows lie in one scale block, its up rows in another; rows past the last read zeros
       const float* s13 = a.s13 + (size_t)r.groups[grp].expert * rb * nkb;
       const int row = min(c0, a.I - 16);
-      ScaleRow sg, su;
-      sg.start(s13 + (size_t)(row / kBlock) * nkb, nkb, b0, lane);
-      su.start(s13 + (size_t)((a.I + row) / kBlock) * nkb, nkb, b0, lane);
+      HalfScales sw;
+      sw.start(s13 + (size_t)((lane < 16 ? row : a.I + row) / kBlock) * nkb, nkb, b0, lane);
       auto run = [&](auto form) {
         constexpr int P = decltype(form)::value;
         float acc[P] = {};
         for (int b = b0; b < b1; ++b) {
-          const float g = sg.at(b, lane), u = su.at(b, lane);
-          if (!add_unit<kUpTerms, P>(bars, p, tmem_lane, C::kCols, scale[p.s], lane < 16 ? g : u, acc, deadline,
-                                     lane)) {
-            bars.give_up(a.err);
-            return;
-          }
+          const float s = sw.at(b, lane);
+          add_unit<kUpTerms, P>(bars, p, seen, tmem_lane, C::kCols, scale[p.s], s, acc, a.err, lane);
         }
         if (S == 1) {
           const int col = c0 + (lane & 15);
@@ -610,7 +654,7 @@ __global__ void __launch_bounds__(kMoeThreads, G == kSmallGroup ? 2 : 1)
           for (int t = 0; t < P; t += 2) {  // the lower lanes finish token t, the upper ones t + 1
             const float other = __shfl_xor_sync(0xffffffffu, lane < 16 ? acc[t + 1] : acc[t], 16);
             const int n = t + (lane >> 4);
-            if (n < np && col < a.I)
+            if (n < np && col < a.I && !bars.abort)
               a.h[(size_t)r.pairs[p0 + n] * a.I + col] =
                   lane < 16 ? silu_mul(acc[t], other) : silu_mul(other, acc[t + 1]);
           }
@@ -717,15 +761,13 @@ __global__ void __launch_bounds__(kMoeThreads, G == kSmallGroup ? 2 : 1)
   } else if (warp == kSumWarps + 1) {
     if (elect_one()) {
       Pos p;
-      for (int u = u0; u < u1; ++u, p.next()) {
+      bool ready = false;
+      for (int u = u0; u < u1; ++u) {
         const uint32_t idesc = idesc_e4m3(kUnitRows, mma_n(kDownTerms * r.groups[u / nkb].form));
-        if (!mbar_wait(&bars.full[p.s], p.phase, deadline, &bars.abort)) {
+        if (!issue_unit(bars, p, ready, tmem, C::kCols, smem, C::kStageBytes, idesc, deadline)) {
           bars.give_up(a.err);
           break;
         }
-        tc_fence_after();
-        unit_mma(tmem + p.s * C::kCols, smem_u32(smem + p.s * C::kStageBytes), idesc);
-        tc_commit(&bars.done[p.s]);
       }
     }
   } else if (warp >= kFirstFormWarp) {
@@ -748,6 +790,7 @@ __global__ void __launch_bounds__(kMoeThreads, G == kSmallGroup ? 2 : 1)
     }
   } else {
     Pos p;
+    bool seen = false;
     const uint32_t tmem_lane = tmem + ((uint32_t)(warp * 32) << 16);
     auto scales_of = [&](int grp, int b) {
       ScaleRow w;
@@ -766,10 +809,7 @@ __global__ void __launch_bounds__(kMoeThreads, G == kSmallGroup ? 2 : 1)
         float acc[P] = {};
         for (int b = bb; b < be; ++b) {
           const float s = sw.at(b, lane);
-          if (!add_unit<kDownTerms, P>(bars, p, tmem_lane, C::kCols, scale[p.s], s, acc, deadline, lane)) {
-            bars.give_up(a.err);
-            return;
-          }
+          add_unit<kDownTerms, P>(bars, p, seen, tmem_lane, C::kCols, scale[p.s], s, acc, a.err, lane);
         }
         // This thread alone adds to its row's sums, and a group's tokens are different ones: an expert appears
         // once in a token's choices.

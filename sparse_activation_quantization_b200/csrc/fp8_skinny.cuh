@@ -37,10 +37,10 @@ struct SkinnyBars {
   uint64_t full[kStages], done[kStages], empty[kStages];
   uint32_t tmem;
   volatile int abort;
-  __device__ __forceinline__ void init(int full_arrivals) {
+  __device__ __forceinline__ void init(int full_arrivals, int done_arrivals) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&full[s], full_arrivals);
-      mbar_init(&done[s], 1);
+      mbar_init(&done[s], done_arrivals);
       mbar_init(&empty[s], kSumWarps);
     }
     fence_mbar_init();
