@@ -848,12 +848,16 @@ cudaError_t launch_linear(const uint8_t* x, const float* xs, int lds, int T, int
   void* args[] = {&mx, &mw, &a};
   const int nkb = blocks_of(K);
   const long long pair_tiles = (long long)((T + 255) / 256) * ((D + 255) / 256);
-  if (pair_tiles * 2 >= dev->sms && pair_regs_ok()) {
+  const long long tiles = (long long)((T + 127) / 128) * ((D + 127) / 128);
+  // Pairs once 128 x 128 tiles need a second wave.  Measured, pair against tile: 768 x 4096 x 4096 (192 tiles) 21 and
+  // 30 us, 4096 x 1024 x 600 (160) 8.6 and 12.4; 600 x 8192 x 3000 (120) 35 and 28, 512 x 4096 x 4096 (128) 20 and 16.
+  if (tiles > dev->sms && pair_regs_ok()) {
     static bool done[64] = {};
     cudaError_t e = opt_in_smem((const void*)fp8_pair_kernel, Pair::kSmemBytes, done);
     if (e != cudaSuccess) return e;
     CUtensorMap my = mx;  // not used unless rows of Y start on 16-byte boundaries
-    if (a.vec_y && !rows_map(&my, y, (uint64_t)T, (uint64_t)D, (uint64_t)ldy, out_f32 ? 4 : 2, 32)) return cudaErrorInvalidValue;
+    if (a.vec_y && !rows_map(&my, y, (uint64_t)T, (uint64_t)D, (uint64_t)ldy, out_f32 ? 4 : 2, 32))
+      return cudaErrorInvalidValue;
     void* pair_args[] = {&mx, &mw, &my, &a};
     const int pairs = (int)(pair_tiles < dev->sms / 2 ? pair_tiles : dev->sms / 2);
     return launch_pdl((const void*)fp8_pair_kernel, dim3(2 * pairs), dim3(Pair::kThreads), Pair::kSmemBytes, 2, stream,
@@ -862,7 +866,6 @@ cudaError_t launch_linear(const uint8_t* x, const float* xs, int lds, int T, int
   static bool done[64] = {};
   cudaError_t e = opt_in_smem((const void*)fp8_tile_kernel, Tile::kSmemBytes, done);
   if (e != cudaSuccess) return e;
-  const long long tiles = (long long)((T + 127) / 128) * ((D + 127) / 128);
   // the widest cluster with which all reside at once
   static Resident known;
   int s = 8;
