@@ -45,6 +45,7 @@ constexpr int kFormWarps = 4, kFirstFormWarp = kSumWarps + 2;
 constexpr int kMoeWarps = kFirstFormWarp + kFormWarps;
 constexpr int kMoeThreads = 32 * kMoeWarps;
 constexpr int kMaxPairs = kMoeMaxTokens * kMoeMaxTopk;
+constexpr int kUpTerms = 2, kDownTerms = 3;  // E4M3 terms of a value of x and of h
 
 struct MoeArgs {
   const __nv_bfloat16* x;   // [T][H]
@@ -60,6 +61,10 @@ struct MoeArgs {
   int* arrived;             // workspace: down's arrivals [tile][8], zero between calls
   float* partial;           // workspace: down's partial sums [tile][parts][T][128]
   float* h;                 // workspace: [T * topk][I]
+  uint8_t* x_terms;         // workspace, groups of 32 only: terms of x and h and their scales (Terms)
+  uint8_t* h_terms;
+  float* x_scale;
+  float* h_scale;
   long long ldx, ldl, ldy;
   int T, E, topk, H, I, renorm;
   int splits;               // CTAs of a cluster
@@ -168,25 +173,6 @@ __device__ __forceinline__ void choose_any(const MoeArgs& a, int t, int& e, floa
 __device__ __forceinline__ void publish_choice(const MoeArgs& a, int pr, int e, float p) {
   if (a.ids) a.ids[pr] = e;
   if (a.weights) a.weights[pr] = p;
-}
-
-// The choices of every token, a warp each, where they do not fit the first wave of
-// gate-up's own warps.
-constexpr int kChooseWarps = 8;
-__global__ void __launch_bounds__(32 * kChooseWarps) moe_choose_kernel(const MoeArgs a) {
-  pdl_trigger();
-  pdl_wait();
-  const int t = (int)(blockIdx.x * kChooseWarps + (threadIdx.x >> 5)), lane = threadIdx.x & 31;
-  if (t >= a.T) return;
-  int e;
-  float p;
-  choose_any(a, t, e, p);
-  if (lane < a.topk) {
-    const int pr = t * a.topk + lane;
-    a.choice_p[pr] = p;
-    a.choice[pr] = e;
-    publish_choice(a, pr, e, p);
-  }
 }
 
 __device__ __forceinline__ unsigned long long tokens_of(const RoutingScratch& sc, int e) {
@@ -324,6 +310,31 @@ struct Raw8 {
   }
 };
 
+// The terms of eight values of a block whose largest is m, and their scale: the
+// values times 2^(7 - floor(log2 m)), the factor from the exponent field, whose
+// clamp keeps it and its inverse normal numbers.
+template <int J>
+__device__ __forceinline__ float split_terms(float (&v)[8], float m, uint2 (&term)[J]) {
+  const uint32_t ef = max(__float_as_uint(m) >> 23, 20u);
+  const float up = __uint_as_float((261u - ef) << 23);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] *= up;
+#pragma unroll
+  for (int j = 0; j < J; ++j) {
+    const uint32_t c0 = e4m3x4(v[0], v[1], v[2], v[3]), c1 = e4m3x4(v[4], v[5], v[6], v[7]);
+    term[j] = make_uint2(c0, c1);
+    if (j + 1 < J) {
+      const float2 d0 = e4m3x2_to_float(c0), d1 = e4m3x2_to_float(c0 >> 16);
+      const float2 d2 = e4m3x2_to_float(c1), d3 = e4m3x2_to_float(c1 >> 16);
+      v[0] = (v[0] - d0.x) * 16.0f, v[1] = (v[1] - d0.y) * 16.0f;
+      v[2] = (v[2] - d1.x) * 16.0f, v[3] = (v[3] - d1.y) * 16.0f;
+      v[4] = (v[4] - d2.x) * 16.0f, v[5] = (v[5] - d2.y) * 16.0f;
+      v[6] = (v[6] - d3.x) * 16.0f, v[7] = (v[7] - d3.y) * 16.0f;
+    }
+  }
+  return ef == 255u ? INFINITY : __uint_as_float((ef - 7u) << 23);  // an infinity saturates in E4M3: it is in the scale
+}
+
 // Block b of np tokens into a stage's B operand (128-byte swizzle) and scales, by
 // one warp: half a warp per token, eight values a lane, kBatch tokens of each half
 // side by side.  rows(n): token n's row; weights(n): a factor of its scale.
@@ -356,34 +367,12 @@ __device__ __forceinline__ void form_batch(uint8_t* dst, float* scale, int n0, i
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) m[i] = fmaxf(m[i], __shfl_xor_sync(0xffffffffu, m[i], o));
   float sc[kBatch];
+  uint2 term[kBatch][J];
 #pragma unroll
   for (int i = 0; i < kBatch; ++i) {
     const int n = n0 + 2 * i + half;
-    // 2^(7 - floor(log2 m)) from the exponent field; the clamp keeps it and its inverse normal numbers
-    const uint32_t ef = max(__float_as_uint(m[i]) >> 23, 20u);
-    const float up = __uint_as_float((261u - ef) << 23);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) f[i][e] *= up;
-    // an infinity saturates in E4M3: it is in the scale
-    sc[i] = (ef == 255u ? INFINITY : __uint_as_float((ef - 7u) << 23)) * (n < np ? weights(n) : 1.0f);
+    sc[i] = split_terms<J>(f[i], m[i], term[i]) * (n < np ? weights(n) : 1.0f);
   }
-  uint2 term[kBatch][J];
-#pragma unroll
-  for (int j = 0; j < J; ++j)
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      float(&v)[8] = f[i];
-      const uint32_t c0 = e4m3x4(v[0], v[1], v[2], v[3]), c1 = e4m3x4(v[4], v[5], v[6], v[7]);
-      term[i][j] = make_uint2(c0, c1);
-      if (j + 1 < J) {
-        const float2 d0 = e4m3x2_to_float(c0), d1 = e4m3x2_to_float(c0 >> 16);
-        const float2 d2 = e4m3x2_to_float(c1), d3 = e4m3x2_to_float(c1 >> 16);
-        v[0] = (v[0] - d0.x) * 16.0f, v[1] = (v[1] - d0.y) * 16.0f;
-        v[2] = (v[2] - d1.x) * 16.0f, v[3] = (v[3] - d1.y) * 16.0f;
-        v[4] = (v[4] - d2.x) * 16.0f, v[5] = (v[5] - d2.y) * 16.0f;
-        v[6] = (v[6] - d3.x) * 16.0f, v[7] = (v[7] - d3.y) * 16.0f;
-      }
-    }
   if (!ready()) return;
 #pragma unroll
   for (int i = 0; i < kBatch; ++i) {
@@ -411,6 +400,68 @@ __device__ __forceinline__ bool form_columns(uint8_t* dst, float* scale, int np,
     form_batch<J, T, 2>(dst, scale, n0, np, P, b, K, rows, weights, ready);
   else if (np > n0)
     form_batch<J, T, 1>(dst, scale, n0, np, P, b, K, rows, weights, ready);
+  return free;
+}
+
+// Where groups are large, every CTA would form the same columns for each of its
+// tiles: 2000 cycles of a unit at 32 tokens, and the tiles' loads wait for it.
+// Then the terms are formed once, as [row][block][term][128] with a scale per row
+// and block, and only gathered here (measured at 16 experts of 2048 x 768, 64
+// tokens with 8 choices: 84 us formed, GATHERED gathered).
+template <int J, class T>
+__device__ __forceinline__ void store_terms(const T* src, long long ld, int rows, int K, uint8_t* codes, float* scale,
+                                            int cta, int ctas) {
+  const int nkb = blocks_of(K), total = rows * nkb, l16 = threadIdx.x & 15, per = (int)(blockDim.x >> 4);
+  const int here = cta * per + (int)(threadIdx.x >> 4);
+  for (int i0 = here; i0 - (int)((threadIdx.x >> 4) & 1) < total; i0 += ctas * per) {  // uniform over the warp
+    const int i = min(i0, total - 1), row = i / nkb, b = i - row * nkb, k = b * kBlock + l16 * 8;
+    Raw8<T> raw;
+    raw.clear();
+    if (k < K) raw.load(src + (size_t)row * ld + k);
+    float f[8], m = 0.0f;
+    raw.floats(f);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(f[e]));
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    uint2 term[J];
+    const float s = split_terms<J>(f, m, term);
+    if (i0 < total) {
+      if (l16 == 0) scale[i] = s;
+#pragma unroll
+      for (int j = 0; j < J; ++j) *reinterpret_cast<uint2*>(codes + ((size_t)i * J + j) * kBlock + l16 * 8) = term[j];
+    }
+  }
+}
+template <int J, class Rows, class Weights, class Wait>
+__device__ __forceinline__ bool gather_columns(uint8_t* dst, float* scale, int np, int P, int b, int nkb,
+                                               const uint8_t* codes, const float* scales, Rows rows, Weights weights,
+                                               Wait wait) {
+  const int lane = threadIdx.x & 31;
+  constexpr int kChunks = J * kBlock / 16, kBatch = 8;  // 16-byte chunks of a token's block; loads on their way
+  const int total = np * kChunks;
+  const float s = lane < np ? __ldcg(scales + (size_t)rows(lane) * nkb + b) * weights(lane) : 0.0f;
+  bool free = false;
+  for (int i0 = 0; i0 < total; i0 += 32 * kBatch) {
+    uint4 v[kBatch];
+#pragma unroll
+    for (int q = 0; q < kBatch; ++q) {
+      const int i = i0 + 32 * q + lane, n = i / kChunks, c = i - n * kChunks;
+      if (i < total)
+        v[q] = __ldcg(reinterpret_cast<const uint4*>(codes + ((size_t)rows(n) * nkb + b) * (J * kBlock)) + c);
+    }
+    if (!free) {
+      free = __all_sync(0xffffffffu, wait());
+      if (!free) return false;
+      if (lane < np) scale[lane] = s;
+    }
+#pragma unroll
+    for (int q = 0; q < kBatch; ++q) {
+      const int i = i0 + 32 * q + lane, n = i / kChunks, c = i - n * kChunks;
+      if (i < total)
+        *reinterpret_cast<uint4*>(dst + codes_chunk_off((uint32_t)((c >> 3) * P + n), (uint32_t)c & 7)) = v[q];
+    }
+  }
   return free;
 }
 
@@ -543,9 +594,42 @@ __device__ __forceinline__ void moe_teardown(uint32_t tmem) {
   }
 }
 
+// ---------------------------------------------- before gate-up and down ---
+
+// The choices of every token, a warp each, where they do not fit the first wave of
+// gate-up's own warps.
+constexpr int kChooseWarps = 8;
+__global__ void __launch_bounds__(32 * kChooseWarps) moe_choose_kernel(const MoeArgs a) {
+  pdl_trigger();
+  pdl_wait();
+  const int choosers = (a.T + kChooseWarps - 1) / kChooseWarps;
+  if ((int)blockIdx.x >= choosers) {  // the other CTAs: the terms of x
+    store_terms<kUpTerms>(a.x, a.ldx, a.T, a.H, a.x_terms, a.x_scale, (int)blockIdx.x - choosers,
+                          (int)gridDim.x - choosers);
+    return;
+  }
+  const int t = (int)(blockIdx.x * kChooseWarps + (threadIdx.x >> 5)), lane = threadIdx.x & 31;
+  if (t >= a.T) return;
+  int e;
+  float p;
+  choose_any(a, t, e, p);
+  if (lane < a.topk) {
+    const int pr = t * a.topk + lane;
+    a.choice_p[pr] = p;
+    a.choice[pr] = e;
+    publish_choice(a, pr, e, p);
+  }
+}
+// The terms of h, between gate-up and down.
+__global__ void __launch_bounds__(256) moe_terms_kernel(const MoeArgs a) {
+  pdl_trigger();
+  pdl_wait();
+  store_terms<kDownTerms>(a.h, (long long)a.I, a.T * a.topk, a.I, a.h_terms, a.h_scale, (int)blockIdx.x, (int)gridDim.x);
+}
+
 // ---------------------------------------------------------------- gate-up ---
 
-constexpr int kUpTerms = 2, kUpCols = 64;
+constexpr int kUpCols = 64;
 template <int G>
 struct Up : MoeRing<kUpTerms, G, G == kSmallGroup ? 5 : 8> {
   // several CTAs of the small form, and down's beside them, reside on an SM
@@ -616,10 +700,18 @@ __global__ void __launch_bounds__(kMoeThreads, G == kSmallGroup ? 2 : 1)
       for (int b = b0; b < b1; ++b, p.next()) {
         if (turn-- > 0) continue;
         turn = C::kFormers - 1;
-        if (!form_columns<kUpTerms, __nv_bfloat16>(
-                smem + p.s * C::kStageBytes + kUnitBytes, scale[p.s], gr.count, gr.form, b, a.H,
-                [&](int n) { return a.x + (size_t)r.token[gr.first + n] * a.ldx; }, [](int) { return 1.0f; },
-                [&]() { return wait_empty(bars, p, deadline); })) {
+        uint8_t* dst = smem + p.s * C::kStageBytes + kUnitBytes;
+        const auto one = [](int) { return 1.0f; };
+        const auto wait = [&]() { return wait_empty(bars, p, deadline); };
+        bool ok;
+        if constexpr (G == kGroup)
+          ok = gather_columns<kUpTerms>(dst, scale[p.s], gr.count, gr.form, b, nkb, a.x_terms, a.x_scale,
+                                        [&](int n) { return (int)r.token[gr.first + n]; }, one, wait);
+        else
+          ok = form_columns<kUpTerms, __nv_bfloat16>(
+              dst, scale[p.s], gr.count, gr.form, b, a.H,
+              [&](int n) { return a.x + (size_t)r.token[gr.first + n] * a.ldx; }, one, wait);
+        if (!ok) {
           bars.give_up(a.err);
           break;
         }
@@ -700,7 +792,6 @@ __global__ void __launch_bounds__(kMoeThreads, G == kSmallGroup ? 2 : 1)
 
 // ------------------------------------------------------------------- down ---
 
-constexpr int kDownTerms = 3;
 // kBeside: the form that fits an SM beside gate-up's (calls of up to 8 tokens).
 template <int G, bool kBeside>
 struct Down : MoeRing<kDownTerms, G, kBeside ? 4 : (G == kSmallGroup ? 3 : 5)> {
@@ -777,10 +868,18 @@ __global__ void __launch_bounds__(kMoeThreads, G == kSmallGroup ? 2 : 1)
       if ((u - u0) % C::kFormers != warp - kFirstFormWarp) continue;
       const int grp = u / nkb;
       const Group gr = r.groups[grp];
-      if (!form_columns<kDownTerms, float>(
-              smem + p.s * C::kStageBytes + kUnitBytes, scale[p.s], gr.count, gr.form, u - grp * nkb, a.I,
-              [&](int n) { return a.h + (size_t)r.pairs[gr.first + n] * a.I; },
-              [&](int n) { return r.p[r.pairs[gr.first + n]]; }, [&]() { return wait_empty(bars, p, deadline); })) {
+      uint8_t* dst = smem + p.s * C::kStageBytes + kUnitBytes;
+      const auto weight = [&](int n) { return r.p[r.pairs[gr.first + n]]; };
+      const auto wait = [&]() { return wait_empty(bars, p, deadline); };
+      bool ok;
+      if constexpr (G == kGroup)
+        ok = gather_columns<kDownTerms>(dst, scale[p.s], gr.count, gr.form, u - grp * nkb, nkb, a.h_terms, a.h_scale,
+                                        [&](int n) { return (int)r.pairs[gr.first + n]; }, weight, wait);
+      else
+        ok = form_columns<kDownTerms, float>(dst, scale[p.s], gr.count, gr.form, u - grp * nkb, a.I,
+                                             [&](int n) { return a.h + (size_t)r.pairs[gr.first + n] * a.I; }, weight,
+                                             wait);
+      if (!ok) {
         bars.give_up(a.err);
         break;
       }
@@ -919,8 +1018,9 @@ cudaError_t launch_form(MoeArgs& a, const uint8_t* w13, const uint8_t* w2, const
   if (e != cudaSuccess) return e;
   if (!kFew) {
     void* args[] = {&a};
-    e = launch_pdl((const void*)moe_choose_kernel, dim3((a.T + kChooseWarps - 1) / kChooseWarps),
-                   dim3(32 * kChooseWarps), 0, 1, stream, args);
+    const int choosers = (a.T + kChooseWarps - 1) / kChooseWarps;
+    const int terms = G == kGroup ? (a.T * blocks_of(a.H) + 2 * kChooseWarps - 1) / (2 * kChooseWarps) : 0;
+    e = launch_pdl((const void*)moe_choose_kernel, dim3(choosers + terms), dim3(32 * kChooseWarps), 0, 1, stream, args);
     if (e != cudaSuccess) return e;
   }
   // Items if every choice were another expert; with few, clusters share them.
@@ -934,6 +1034,11 @@ cudaError_t launch_form(MoeArgs& a, const uint8_t* w13, const uint8_t* w2, const
   e = launch_pdl(up, dim3((unsigned)((most < resident ? most : resident) * a.splits)), dim3(kMoeThreads),
                  U::kSmemBytes, a.splits, stream, up_args);
   if (e != cudaSuccess) return e;
+  if (G == kGroup) {
+    void* args[] = {&a};
+    e = launch_pdl((const void*)moe_terms_kernel, dim3((pairs * blocks_of(a.I) + 15) / 16), dim3(256), 0, 1, stream, args);
+    if (e != cudaSuccess) return e;
+  }
   // The widest cluster with which every CTA resides at once, and several to a tile where there are few tiles.  With
   // two CTAs on an SM clusters of at most 4: of 8 (and 16) fewer fit, and one that has to wait costs a second wave
   // (45 us at 64 tokens).
@@ -958,7 +1063,9 @@ cudaError_t launch_form(MoeArgs& a, const uint8_t* w13, const uint8_t* w2, const
 
 size_t moe_workspace(int T, int topk, int H, int I) {
   const size_t pairs = (size_t)T * topk, tiles = (size_t)(H + kUnitRows - 1) / kUnitRows;
+  const size_t xb = (size_t)T * blocks_of(H), hb = pairs * blocks_of(I);
   return kFixedBytes + align256(8 * pairs) + align256(pairs * I * sizeof(float)) +
+         align256(xb * (kUpTerms * kBlock + sizeof(float))) + align256(hb * (kDownTerms * kBlock + sizeof(float))) +
          (tiles <= kMaxSharedTiles ? kMaxParts * tiles * T * kUnitRows * sizeof(float) : 0);
 }
 
@@ -984,7 +1091,12 @@ cudaError_t launch_moe(const void* x, long long ldx, const float* logits, long l
   a.choice = reinterpret_cast<int*>(at += kFixedBytes);
   a.choice_p = reinterpret_cast<float*>(a.choice + pairs);
   a.h = reinterpret_cast<float*>(at += align256(8 * pairs));
-  a.partial = reinterpret_cast<float*>(at += align256(pairs * I * sizeof(float)));
+  a.x_terms = at += align256(pairs * I * sizeof(float));
+  const size_t xb = (size_t)T * blocks_of(H), hb = pairs * blocks_of(I);
+  a.x_scale = reinterpret_cast<float*>(a.x_terms + xb * kUpTerms * kBlock);
+  a.h_terms = at += align256(xb * (kUpTerms * kBlock + sizeof(float)));
+  a.h_scale = reinterpret_cast<float*>(a.h_terms + hb * kDownTerms * kBlock);
+  a.partial = reinterpret_cast<float*>(at += align256(hb * (kDownTerms * kBlock + sizeof(float))));
   a.parts = 1;
   a.ldx = ldx;
   a.ldl = ldl;
