@@ -1,5 +1,6 @@
-// fp8_moe.cu - a whole mixture-of-experts layer for a few tokens: two kernels, and
-// one that chooses the experts above 8 tokens.
+// fp8_moe.cu - a whole mixture-of-experts layer for a few tokens: two kernels up to
+// 8 tokens, one more that chooses the experts above, and with more than 4 tokens
+// an expert on average one that prepares h between the two.
 //
 //   chosen(t) = the k largest router logits of token t (ties: lower index)
 //   p(t, j)   = softmax of the logits over the chosen (or over all) experts
@@ -25,7 +26,8 @@
 //   down     a cluster of CTAs owns 128 rows of W_down for all tokens; each CTA
 //            takes a share of the (group, k block) units and sums p * result per
 //            token in shared memory; the CTAs' sums are joined in rank order over
-//            distributed shared memory.
+//            distributed shared memory.  Where there are few row tiles several
+//            clusters share one, and the last of them adds their parts in order.
 // Warps of a CTA: 0-3 sums, 4 copies (one thread), 5 MMAs (one thread) and TMEM,
 // 6-9 form the columns, a unit each in turn.  Up to 8 tokens every CTA chooses their
 // experts itself, a warp per token; above that a small kernel does it before (64
@@ -407,7 +409,7 @@ __device__ __forceinline__ bool form_columns(uint8_t* dst, float* scale, int np,
 // tiles: 2000 cycles of a unit at 32 tokens, and the tiles' loads wait for it.
 // Then the terms are formed once, as [row][block][term][128] with a scale per row
 // and block, and only gathered here (measured at 16 experts of 2048 x 768, 64
-// tokens with 8 choices: 84 us formed, GATHERED gathered).
+// tokens with 8 choices: 84 us formed, 61 us gathered).
 template <int J, class T>
 __device__ __forceinline__ void store_terms(const T* src, long long ld, int rows, int K, uint8_t* codes, float* scale,
                                             int cta, int ctas) {
@@ -624,7 +626,8 @@ __global__ void __launch_bounds__(32 * kChooseWarps) moe_choose_kernel(const Moe
 __global__ void __launch_bounds__(256) moe_terms_kernel(const MoeArgs a) {
   pdl_trigger();
   pdl_wait();
-  store_terms<kDownTerms>(a.h, (long long)a.I, a.T * a.topk, a.I, a.h_terms, a.h_scale, (int)blockIdx.x, (int)gridDim.x);
+  store_terms<kDownTerms>(a.h, (long long)a.I, a.T * a.topk, a.I, a.h_terms, a.h_scale, (int)blockIdx.x,
+                          (int)gridDim.x);
 }
 
 // ---------------------------------------------------------------- gate-up ---
@@ -1036,7 +1039,8 @@ cudaError_t launch_form(MoeArgs& a, const uint8_t* w13, const uint8_t* w2, const
   if (e != cudaSuccess) return e;
   if (G == kGroup) {
     void* args[] = {&a};
-    e = launch_pdl((const void*)moe_terms_kernel, dim3((pairs * blocks_of(a.I) + 15) / 16), dim3(256), 0, 1, stream, args);
+    e = launch_pdl((const void*)moe_terms_kernel, dim3((pairs * blocks_of(a.I) + 15) / 16), dim3(256), 0, 1, stream,
+                   args);
     if (e != cudaSuccess) return e;
   }
   // The widest cluster with which every CTA resides at once, and several to a tile where there are few tiles.  With

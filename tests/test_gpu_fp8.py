@@ -564,6 +564,20 @@ def test_moe_strides_and_in_place():
     assert (xb[6] == 5.0).all() and (xb[:, 256:] == 5.0).all()
 
 
+@pytest.mark.parametrize("T,E", [(20, 40), (20, 3), (64, 4)])
+def test_moe_strides_and_in_place_above_eight_tokens(T, E):
+    x, lg, w13, s13, w2, s2 = moe_inputs(T, E, 272, 144, 13)
+    xb = torch.full((T + 1, 288), 5.0, dtype=torch.bfloat16, device="cuda")
+    xb[:T, :272] = x.cuda()
+    lb = torch.full((T, E + 3), 1e9, device="cuda")
+    lb[:, :E] = lg.cuda()
+    a, b = sq.Fp8Weight.from_parts(w13.cuda(), s13.cuda()), sq.Fp8Weight.from_parts(w2.cuda(), s2.cuda())
+    xin = xb[:T, :272]
+    out = sq.fp8_moe(xin, lb[:, :E], a, b, 2, out=xin, return_routing=True)
+    check_moe(out, x, lg, w13, s13, w2, s2, 2)
+    assert (xb[T] == 5.0).all() and (xb[:, 272:] == 5.0).all()
+
+
 def test_moe_refusals():
     x, lg, w13, s13, w2, s2 = (t.cuda() for t in moe_inputs(4, 8, 256, 64, 1))
     a, b = sq.Fp8Weight.from_parts(w13, s13), sq.Fp8Weight.from_parts(w2, s2)
