@@ -77,7 +77,10 @@ struct MoeArgs {
 // t * topk + j that chose it, cut into groups of at most G tokens.  G = 8 for
 // calls of up to 8 tokens, whose groups never hold more.
 constexpr int kSmallGroup = 8, kGroup = 32;
-constexpr int kMaxGroups = kMoeMaxExperts + kMaxPairs / kGroup;
+// n experts that P pairs chose are at most n + (P - n) / G groups: one each, and one more for every G further tokens.
+// That grows with n and is largest for the smaller G, with every expert chosen.
+constexpr int kMaxGroups = kMoeMaxExperts + (kMaxPairs - kMoeMaxExperts) / kSmallGroup;
+static_assert(kSmallGroup <= kGroup && kMoeMaxExperts <= kMaxPairs, "the bound above");
 struct Group {
   short expert, first, count, form;  // first of its pairs, their number, tokens_form of it
 };
@@ -560,8 +563,8 @@ struct MoeRing {
   static_assert(kTmem <= 512 && kStageBytes % 1024 == 0, "ring");
 };
 
-// Where part i of n begins among `total`.  In 32 bits: at most 544 groups of 2048
-// column tiles or 1024 k blocks, and a few hundred CTAs.
+// Where part i of n begins among `total`.  In 32 bits: at most kMaxGroups (576)
+// groups of 2048 column tiles or 1024 k blocks, and a few hundred CTAs.
 __device__ __forceinline__ int share_of(int i, int total, int n) {
   return (int)((uint32_t)i * (uint32_t)total / (uint32_t)n);
 }
@@ -804,6 +807,9 @@ struct Down : MoeRing<kDownTerms, G, kBeside ? 4 : (G == kSmallGroup ? 3 : 5)> {
 using BesideDown = Down<kSmallGroup, true>;
 static_assert(Up<kSmallGroup>::kSmemBytes + BesideDown::bytes(kSmallGroup) + 2 * (int)sizeof(Routing) <= 226 * 1024 &&
               Up<kSmallGroup>::kTmem + BesideDown::kTmem <= 512, "both kernels' forms share an SM");
+static_assert(2 * (Up<kSmallGroup>::kSmemBytes + (int)sizeof(Routing) + 2048) <= 226 * 1024 &&
+              2 * (Down<kSmallGroup, false>::bytes(kMoeMaxTokens) + (int)sizeof(Routing) + 2048) <= 226 * 1024,
+              "two CTAs of the small forms, with 2 KB of barriers and scales each, share an SM");
 
 template <int G, bool kBeside>
 __global__ void __launch_bounds__(kMoeThreads, G == kSmallGroup ? 2 : 1)

@@ -1,0 +1,41 @@
+"""The 8-bit path at the ends of what its calls accept (GPU), against oracle/fp8.py with the bounds of
+tests/test_gpu_fp8.py."""
+import numpy as np
+import pytest
+import torch
+
+import sparse_activation_quantization_b200 as sq
+from tests import gpu_helpers as H
+from tests.test_fp8_limits_host import groups_of, skewed_choices
+from tests.test_gpu_fp8 import check_moe, moe_inputs
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    H.ensure_built()
+
+
+def fp8_moe(x, lg, w13, s13, w2, s2, topk, **kw):
+    """fp8_moe with a workspace of its own, whose error word is read"""
+    a, b = sq.Fp8Weight.from_parts(w13.cuda(), s13.cuda()), sq.Fp8Weight.from_parts(w2.cuda(), s2.cuda())
+    ws = sq.Fp8Workspace.for_moe(x.shape[0], topk, a, b)
+    out = sq.fp8_moe(x.cuda(), lg.cuda(), a, b, topk, ws=ws, return_routing=True, **kw)
+    assert ws.check() == 0
+    return out
+
+
+@pytest.mark.parametrize("topk", [13, 16])
+@pytest.mark.parametrize("Hd,I", [(128, 32), (272, 80)])
+def test_moe_routing_with_the_most_groups(topk, Hd, I):
+    """64 tokens over all of 512 experts, 64 of them chosen by nine tokens (topk = 16): groups of 8, 576 of them"""
+    x, lg, *w = moe_inputs(64, 512, Hd, I, 21)
+    ids = torch.from_numpy(skewed_choices())
+    lg = (lg * 0.25).clamp(-4, 4)
+    lg.scatter_(1, ids, lg.gather(1, ids) + 10)
+    assert topk < 16 or groups_of(np.bincount(lg.topk(topk).indices.reshape(-1), minlength=512), 8) == 576
+    out = fp8_moe(x, lg, *w, topk)
+    check_moe(out, x, lg, *w, topk)
+    again = fp8_moe(x, lg, *w, topk)
+    assert all(torch.equal(a, b) for a, b in zip(out, again))
