@@ -71,13 +71,13 @@ __device__ __forceinline__ void load8(const PrepArgs& a, int t, int c, float (&v
 
 // Scales and codes of R 128-blocks that 16 neighbouring lanes hold, 8 values of
 // each a lane: block i is row t[i], this lane's columns c[i] .. c[i] + 7 (c >= K:
-// zeros, nothing stored), its values v[i] mul.  The maxima are reduced and
+// zeros, nothing stored), its values v[i].  The maxima are reduced and
 // handed out at once: in each step a lane gives away half of its blocks, so R - 1
 // exchanges leave a block to every 16 / R lanes, whose scale and reciprocal are
 // then computed once and not by every lane for every block.
 template <int R>
 __device__ __forceinline__ void quant_blocks(const PrepArgs& a, const int (&t)[R], const int (&c)[R],
-                                             const float (&v)[R][8], float mul) {
+                                             const float (&v)[R][8]) {
   static_assert(R == 1 || R == 2 || R == 4, "blocks");
   constexpr int kLanes = 16 / R;  // that share a block at the end
   const int l16 = threadIdx.x & 15;
@@ -102,19 +102,15 @@ __device__ __forceinline__ void quant_blocks(const PrepArgs& a, const int (&t)[R
       m[0] = fmaxf(m[0], __shfl_xor_sync(0xffffffffu, m[0], o));
     }
   }
-  const float s = block_scale_e4m3(m[0] * mul);  // of block l16 / kLanes
+  const float s = block_scale_e4m3(m[0]);  // of block l16 / kLanes
   const float inv = __frcp_rn(s);
-  // v (mul / s), or (v mul) / s where the factor leaves float32: a block whose largest is below 2^-117 in a row whose
-  // root mean square is below 1/4
-  const bool split = __any_sync(0xffffffffu, !(inv * mul < INFINITY));
-  const float first = split ? mul : 1.0f, then = split ? inv : inv * mul;
 #pragma unroll
   for (int i = 0; i < R; ++i) {
-    const float k = R == 1 ? then : __shfl_sync(0xffffffffu, then, (threadIdx.x & 16) | (i * kLanes));
+    const float k = R == 1 ? inv : __shfl_sync(0xffffffffu, inv, (threadIdx.x & 16) | (i * kLanes));
     if (c[i] < a.K) {
       float q[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) q[e] = split ? v[i][e] * first * k : v[i][e] * k;
+      for (int e = 0; e < 8; ++e) q[e] = v[i][e] * k;
       *reinterpret_cast<uint2*>(a.codes + (size_t)t[i] * a.K + c[i]) =
           make_uint2(e4m3x4(q[0], q[1], q[2], q[3]), e4m3x4(q[4], q[5], q[6], q[7]));
     }
@@ -161,7 +157,7 @@ __global__ void __launch_bounds__(256, kQuantCtas) fp8_quant_kernel(const PrepAr
       for (int e = 0; e < 8; ++e) v[u][e] = 0.0f;
       if (rc[u] < a.K) values8<kKind>(a, rt[u], rc[u], raw[u], v[u]);
     }
-    quant_blocks<kUnroll>(a, rt, rc, v, 1.0f);
+    quant_blocks<kUnroll>(a, rt, rc, v);
   }
 }
 
@@ -188,7 +184,9 @@ __device__ __noinline__ double inv_rms_wide(double s2, const PrepArgs& a) {
 constexpr int kWideThreads = 640;
 
 // With a norm, one CTA (or one warp) holds a row: R vectors of 8 columns per
-// thread, as bf16.  kWarpRow: a warp per row, no barrier.
+// thread, as bf16.  kWarpRow: a warp per row, no barrier.  The products are
+// taken from left to right, (x / rms) gamma: x gamma may leave float32 where
+// neither x / rms nor the result does.
 template <int kKind, int R, bool kWarpRow, int kThreads, int kCtas>
 __global__ void __launch_bounds__(kThreads, kCtas) fp8_norm_kernel(const PrepArgs a) {
   __shared__ float part[32];
@@ -255,10 +253,10 @@ __global__ void __launch_bounds__(kThreads, kCtas) fp8_norm_kernel(const PrepArg
         float g[8];
         unpack_bf16x8(*reinterpret_cast<const uint4*>(a.gamma + rc[i]), g);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[i][e] = (fits ? v[i][e] : (float)((double)v[i][e] * inv2)) * g[e];
+        for (int e = 0; e < 8; ++e) v[i][e] = (fits ? v[i][e] * inv : (float)((double)v[i][e] * inv2)) * g[e];
       }
     }
-    quant_blocks<G>(a, rt, rc, v, fits ? inv : 1.0f);
+    quant_blocks<G>(a, rt, rc, v);
   }
 }
 
@@ -314,7 +312,7 @@ __global__ void __launch_bounds__(1024) fp8_norm_long_kernel(const PrepArgs a) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[i] = (fits ? v[i] * (float)inv : (float)((double)v[i] * inv)) * g[i];
     }
-    quant_blocks<1>(a, {t}, {c}, reinterpret_cast<const float(&)[1][8]>(v), 1.0f);
+    quant_blocks<1>(a, {t}, {c}, reinterpret_cast<const float(&)[1][8]>(v));
   }
 }
 

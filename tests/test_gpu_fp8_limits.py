@@ -5,9 +5,10 @@ import pytest
 import torch
 
 import sparse_activation_quantization_b200 as sq
+from oracle import fp8 as O
 from tests import gpu_helpers as H
 from tests.test_fp8_limits_host import groups_of, skewed_choices
-from tests.test_gpu_fp8 import check_moe, moe_inputs
+from tests.test_gpu_fp8 import check_moe, check_quant, check_untouched, make_act, moe_inputs, norm_delta
 
 pytestmark = pytest.mark.gpu
 
@@ -39,3 +40,25 @@ def test_moe_routing_with_the_most_groups(topk, Hd, I):
     check_moe(out, x, lg, *w, topk)
     again = fp8_moe(x, lg, *w, topk)
     assert all(torch.equal(a, b) for a, b in zip(out, again))
+
+
+@pytest.mark.parametrize("residual", [False, True])
+@pytest.mark.parametrize("T,K,x_exp,gamma_exp", [
+    (3, 64, 56, 74), (3, 64, -45, -110),         # a warp per row
+    (3, 2064, 54, 76), (3, 2064, -48, -105),     # a vector per thread
+    (160, 1040, 54, 76), (160, 1040, -47, -106),  # four vectors per thread
+    (2, 33008, 50, 80), (2, 33008, -50, -105),   # rows that are read twice
+])
+def test_prep_norm_before_gamma(T, K, x_exp, gamma_exp, residual):
+    """x * (1 / rms) * gamma from left to right: x * gamma leaves float32, x / rms and the result do not"""
+    g = np.random.default_rng(T + K)
+    x = torch.from_numpy(((g.random((T, K)) + 1) * g.choice([-1.0, 1.0], (T, K)) * 2.0 ** x_exp).astype(np.float32))
+    gamma = torch.from_numpy(((g.random(K) + 0.5) * 2.0 ** gamma_exp).astype(np.float32))
+    x, gamma = x.bfloat16(), gamma.bfloat16()
+    act, codes, scales = make_act(T, K)
+    if residual:
+        act.prep_residual(x.cuda(), torch.zeros_like(x).cuda(), None, gamma.cuda(), 0.0)
+    else:
+        act.prep(x.cuda(), gamma.cuda(), 0.0)
+    check_quant(act, O.rms_norm(x.float().numpy(), gamma.float().numpy(), 0.0), norm_delta(K))
+    check_untouched(act, codes, scales)
