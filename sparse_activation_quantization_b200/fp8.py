@@ -92,6 +92,8 @@ def _vector(name, t, n, dtype, device):
 
 def _device(device):
     device = torch.device(device)
+    if device.type != "cuda":
+        raise ValueError(f"buffers lie on a CUDA device, got {device}")
     return torch.device("cuda", torch.cuda.current_device()) if device.index is None else device
 
 

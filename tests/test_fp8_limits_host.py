@@ -61,3 +61,14 @@ def test_moe_group_table_holds_every_routing(E):
             small = T <= c["kSmallGroup"] or T * topk <= 4 * E  # launch_moe
             size = c["kSmallGroup"] if small else c["kGroup"]
             assert most_groups(T, topk, E, size) <= c["kMaxGroups"]
+
+
+@pytest.mark.parametrize("device", ["cpu", "cpu:0", "meta"])
+def test_buffers_are_cuda_buffers(device):
+    """a kernel would be given the address of host memory"""
+    from sparse_activation_quantization_b200 import build
+    build.build()
+    for make in (lambda: sq.Fp8Act(4, 256, device=device), lambda: sq.Fp8Workspace(256, device=device),
+                 lambda: sq.Fp8Workspace.for_linear(4, 256, 256, device=device)):
+        with pytest.raises(ValueError, match="CUDA device"):
+            make()
