@@ -170,8 +170,8 @@ class Fp8Act:
     def from_parts(cls, codes, scales):
         """Codes float8_e4m3fn [T, K] and scales float32 [T, ceil(K/128)] from
         elsewhere.  Scales stored column by column (stride(0) == 1, stride(1) a
-        multiple of 4, the last column as long as the others) are used as they
-        are, others are copied."""
+        multiple of 4 below 2^31, the last column as long as the others) are
+        used as they are, others are copied."""
         _cuda("codes", codes, _F8)
         _cuda("scales", scales, torch.float32, codes.device)
         if codes.dim() != 2 or scales.shape != (codes.shape[0], _blocks(codes.shape[1])):
@@ -182,7 +182,7 @@ class Fp8Act:
         codes = codes.contiguous()
         lds = scales.stride(1)
         behind = scales.untyped_storage().nbytes() // 4 - scales.storage_offset()  # floats from the first scale on
-        if (T > 1 and scales.stride(0) != 1) or lds < T or lds % 4 or scales.data_ptr() % 16 or \
+        if (T > 1 and scales.stride(0) != 1) or lds < T or lds % 4 or lds >= 1 << 31 or scales.data_ptr() % 16 or \
                 behind < _blocks(K) * lds:
             lds = -(-T // 4) * 4
             own = scales.new_empty(_blocks(K), lds)

@@ -8,7 +8,8 @@ import sparse_activation_quantization_b200 as sq
 from oracle import fp8 as O
 from tests import gpu_helpers as H
 from tests.test_fp8_limits_host import groups_of, skewed_choices
-from tests.test_gpu_fp8 import check_moe, check_quant, check_untouched, make_act, moe_inputs, norm_delta
+from tests.test_gpu_fp8 import (check_linear, check_moe, check_quant, check_untouched, linear_reference, make_act,
+                                moe_inputs, norm_delta, operands)
 
 pytestmark = pytest.mark.gpu
 
@@ -62,3 +63,20 @@ def test_prep_norm_before_gamma(T, K, x_exp, gamma_exp, residual):
         act.prep(x.cuda(), gamma.cuda(), 0.0)
     check_quant(act, O.rms_norm(x.float().numpy(), gamma.float().numpy(), 0.0), norm_delta(K))
     check_untouched(act, codes, scales)
+
+
+def test_scale_columns_further_apart_than_32_bits_say():
+    """the struct holds the distance of two columns as an int: beyond that the scales are copied"""
+    far = 2 ** 32 + 4
+    x, xs, w, ws = operands(4, 256, 40, 7)
+    big = torch.empty(2 * far, device="cuda")
+    scales = big.as_strided((4, 2), (1, far))
+    scales.copy_(xs)
+    big[4:8] = -1.0  # where a distance cut to 32 bits would look
+    act = sq.Fp8Act.from_parts(x.cuda(), scales)
+    assert act.scales.data_ptr() != big.data_ptr() and torch.equal(act.scales.cpu(), xs)
+    y = sq.fp8_linear(act, sq.Fp8Weight.from_parts(w.cuda(), ws.cuda()))
+    ref, bound = linear_reference(x, xs, w, ws)
+    check_linear(y, ref, bound, torch.bfloat16)
+    del big, scales
+    torch.cuda.empty_cache()
