@@ -15,7 +15,10 @@ namespace fp8 {
 
 constexpr int kBlock = 128;                 // elements (and weight columns) per scale
 constexpr float kE4m3Max = 448.0f;
-constexpr uint64_t kWaitNs = 4000000000ull;  // bound of every device-side wait: far beyond any tile's work
+// Bound of a device-side wait, far beyond any tile's work.  Copy, MMA and forming warps count it from the start of the
+// kernel (of the tile in the pair kernel; twice it in the expert layer's down, beside gate-up), sum warps from the start
+// of each wait.  A kernel whose wait has run out leaves within a few of them.
+constexpr uint64_t kWaitNs = 4000000000ull;
 constexpr int kErrTimeoutWord = -5;          // SHARQ_ERR_TIMEOUT
 
 __host__ __device__ __forceinline__ int blocks_of(int n) { return (n + kBlock - 1) / kBlock; }
@@ -112,15 +115,25 @@ __device__ __forceinline__ void mbar_arrive_cta(uint64_t* bar) {
   asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
-// Bounded wait without a clock: the number of tries is limited instead (each
-// takes 20 cycles or more, and up to about a microsecond while the phase is
-// open), which leaves no 64-bit deadline in registers.  70 cycles less a wait in
-// a loop that is short of them.
+// The same wait for loops that are short of registers: no 64-bit deadline is
+// carried through them (70 cycles a wait).  The low half of the timer is read
+// when the first try has run out, and kWaitNs lies below its period of 2^32 ns.
+__device__ __forceinline__ uint32_t globaltimer_lo() {
+  uint32_t t;
+  asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t));
+  return t;
+}
 __device__ __forceinline__ bool mbar_wait_short(uint64_t* bar, uint32_t parity, volatile int* abort) {
-  for (uint32_t n = 0; !mbar_try_wait(bar, parity); ++n)
-    if (*abort || n == (1u << 27)) return false;
+  static_assert(kWaitNs < 1ull << 32, "the bound in 32 bits");
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint32_t start = globaltimer_lo();
+  while (!mbar_try_wait(bar, parity))
+    if (*abort || globaltimer_lo() - start > (uint32_t)kWaitNs) return false;
   return true;
 }
+// Whether the CTA has given up, the same answer for every lane: for loops of
+// whole warps, whose shuffles and TMEM reads no lane may leave alone.
+__device__ __forceinline__ bool warp_stopped(volatile int* abort) { return __any_sync(0xffffffffu, *abort); }
 // whether the phase of parity `parity` is complete, without waiting for it
 __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
   uint32_t ok;

@@ -182,7 +182,7 @@ __global__ void __launch_bounds__(Skinny<kN>::kThreads, 2)
     }
   } else {
     RingPos<C::kStages> p;
-    for (int tile = first; tile < tiles && !bars.abort; tile += step) {
+    for (int tile = first; tile < tiles && !warp_stopped(&bars.abort); tile += step) {
       ScaleRow ws;
       ws.start(a.ws + (size_t)tile * nkb, nkb, b0, lane);
 #pragma unroll
@@ -762,8 +762,9 @@ __global__ void __launch_bounds__(Pair::kThreads, 1)
         }
       }
       next_tile(w);
+      if (warp_stopped(&abort_sh)) break;
       if (w.tile < ntiles) scales(w);  // on their way while this tile is stored
-      if (row0 < a.T && col0 < a.D && !abort_sh) {
+      if (row0 < a.T && col0 < a.D) {
         uint32_t o[32];
         if (lane == 0) bulk_wait_read_all();  // the last tile's stores have left the staging area
         __syncwarp();

@@ -701,7 +701,7 @@ __global__ void __launch_bounds__(kMoeThreads, G == kSmallGroup ? 2 : 1)
     Pos p;
     static_assert(C::kFormers == kFormWarps, "every former has a turn");
     int turn = warp - kFirstFormWarp;  // units until this warp's next
-    for (int it = it0; it < it1 && !bars.abort; ++it) {
+    for (int it = it0; it < it1 && !warp_stopped(&bars.abort); ++it) {
       const Group gr = r.groups[it / tiles];
       for (int b = b0; b < b1; ++b, p.next()) {
         if (turn-- > 0) continue;
@@ -731,7 +731,8 @@ __global__ void __launch_bounds__(kMoeThreads, G == kSmallGroup ? 2 : 1)
     bool seen = false;
     const int rb = blocks_of(2 * a.I);
     const uint32_t tmem_lane = tmem + ((uint32_t)(warp * 32) << 16);
-    for (int it = it0; it < it1 && !bars.abort; ++it) {
+    // with S > 1 every sum warp has to come to its item's barrier
+    for (int it = it0; it < it1 && (S > 1 || !warp_stopped(&bars.abort)); ++it) {
       const int grp = it / tiles, c0 = (it - grp * tiles) * kUpCols + 16 * warp;
       const int np = r.groups[grp].count, p0 = r.groups[grp].first;
       // the warp's 16 gate rows lie in one scale block, its up rows in another; rows past the last read zeros
@@ -907,7 +908,7 @@ __global__ void __launch_bounds__(kMoeThreads, G == kSmallGroup ? 2 : 1)
     };
     ScaleRow ahead;
     if (u0 < u1) ahead = scales_of(u0 / nkb, u0 % nkb);
-    for (int u = u0; u < u1 && !bars.abort;) {
+    for (int u = u0; u < u1 && !warp_stopped(&bars.abort);) {
       const int grp = u / nkb, bb = u - grp * nkb, be = min(nkb, bb + u1 - u);
       const int np = r.groups[grp].count, p0 = r.groups[grp].first;
       ScaleRow sw = ahead;
