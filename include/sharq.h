@@ -477,8 +477,9 @@ int sharq_fp8_linear(const sharq_fp8_act *a, const sharq_fp8_weight *w, void *d_
  * w13: E experts of D = 2 I rows, the gate's I rows and then the up's, K = H;
  * w2: E experts of D = H, K = I.  d_X: bf16 [T][H], row stride ldx; activations
  * are not quantized: x enters as two E4M3 terms of a power-of-two scale per 128
- * (exact down to 2^-13 of the block's largest), h (float32) as three (2^-12
- * relative).  An expert of weight 0 is not evaluated, so a masked token's x may
+ * (exact down to 2^-13 of the block's largest, below that off by 2^-21 of that
+ * largest), h (float32) as three (off by 2^-12 of itself or by 2^-25 of its
+ * 128-block's largest, whichever is more).  An expert of weight 0 is not evaluated, so a masked token's x may
  * hold anything.  d_Y: bf16 [T][H], row stride ldy; it may be d_X.  d_topk_ids
  * (int32) and d_topk_weights (float32), [T][topk]: written unless NULL.
  * T <= 64, topk <= 16 and <= E, E <= 512 (SHARQ_ERR_UNSUPPORTED_SHAPE).

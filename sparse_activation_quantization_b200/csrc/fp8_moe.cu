@@ -17,7 +17,8 @@
 // MMA's B operand of its own, and the columns of a token are added at the end
 // with its power of two.  Four bits a term: two terms hold a bf16 activation
 // exactly where it is at least 2^-13 of the block's largest, and to 2^-21 of that
-// largest below; three hold h to 2^-12 of itself.
+// largest below; three hold h to 2^-12 of itself or 2^-25 of its block's largest,
+// whichever is more (half the spacing of the last term's smallest numbers).
 //   gate-up  item = (group of tokens of one expert, 64 columns of h): the unit's
 //            128 rows are 16 gate rows, the 16 up rows of the same columns, and so
 //            on, so gate and up of a column meet in one warp.  Each CTA walks a

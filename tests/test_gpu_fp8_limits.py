@@ -8,8 +8,8 @@ import sparse_activation_quantization_b200 as sq
 from oracle import fp8 as O
 from tests import gpu_helpers as H
 from tests.test_fp8_limits_host import groups_of, skewed_choices
-from tests.test_gpu_fp8 import (check_linear, check_moe, check_quant, check_untouched, linear_reference, make_act,
-                                moe_inputs, norm_delta, operands)
+from tests.test_gpu_fp8 import (F8, check_linear, check_moe, check_quant, check_untouched, f64, linear_reference,
+                                make_act, moe_inputs, norm_delta, operands)
 
 pytestmark = pytest.mark.gpu
 
@@ -80,3 +80,28 @@ def test_scale_columns_further_apart_than_32_bits_say():
     check_linear(y, ref, bound, torch.bfloat16)
     del big, scales
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("T,E", [(1, 1), (12, 4), (64, 1)])  # one token; groups of 8; groups of 32
+def test_moe_h_of_one_block_from_large_to_small(T, E):
+    """y = h through a unit w2: h is off by 2^-12 of itself or 2^-25 of its block's largest, and bf16 (8 significant bits,
+    so a spacing of 2^-7 from 1 to 2) by half a spacing, 2^-8 of itself"""
+    n = 128
+    x = torch.zeros(T, n, dtype=torch.bfloat16)
+    x[:, 0] = 1.0
+    w13 = torch.zeros(E, 2 * n, n)
+    w13[:, :n, 0] = torch.exp2(torch.arange(n) % 13 - 9.0)             # gates from 2^-9 to 8
+    w13[:, n:, 0] = torch.exp2(torch.arange(n) // 8 - 8.0) * 1.125     # up from 2^-8 to 2^7
+    one13, one2 = torch.ones(E, 2, 1), torch.ones(E, 1, 1)
+    w2 = torch.eye(n).repeat(E, 1, 1)
+    lg = torch.full((T, E), -100.0)
+    lg[:, 0] = 100.0
+    y, ids, p = fp8_moe(x, lg, w13.to(F8), one13, w2.to(F8), one2, 1)
+    assert (ids == 0).all() and (p == 1).all()
+    v = f64(w13.to(F8)[0, :, 0])  # what the codes hold: 1.125 * 2^-8 lies between two of E4M3's smallest numbers
+    h = O.silu(v[:n]) * v[n:]
+    assert h.max() / h.min() > 2.0 ** 25
+    own = np.maximum(2.0 ** -12 * np.abs(h), 2.0 ** -25 * np.abs(h).max()) + 2.0 ** -18 * np.abs(h)  # and silu, float32 sums
+    err = np.abs(f64(y) - h)
+    assert (err <= own + 2.0 ** -8 * (np.abs(h) + own)).all()
+    assert (err > 2.0 ** -11 * np.abs(h) + 2.0 ** -8 * np.abs(h)).any()  # so 2^-12 of itself alone does not hold
