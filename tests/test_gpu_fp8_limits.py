@@ -1,17 +1,24 @@
 """The 8-bit path at the ends of what its calls accept (GPU), against oracle/fp8.py with the bounds of
 tests/test_gpu_fp8.py."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
 
 import sparse_activation_quantization_b200 as sq
+import synthetic
 from oracle import fp8 as O
 from tests import gpu_helpers as H
+from tests.gpu_helpers import bf16_dev as bf
 from tests.test_fp8_limits_host import groups_of, skewed_choices
-from tests.test_gpu_fp8 import (F8, check_linear, check_moe, check_quant, check_untouched, f64, linear_reference,
+from tests.test_gpu_fp8 import (F8, Layer, check_linear, check_moe, check_quant, check_untouched, f64, linear_reference,
                                 make_act, moe_inputs, norm_delta, operands)
 
 pytestmark = pytest.mark.gpu
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -105,3 +112,152 @@ def test_moe_h_of_one_block_from_large_to_small(T, E):
     err = np.abs(f64(y) - h)
     assert (err <= own + 2.0 ** -8 * (np.abs(h) + own)).all()
     assert (err > 2.0 ** -11 * np.abs(h) + 2.0 ** -8 * np.abs(h)).any()  # so 2^-12 of itself alone does not hold
+
+
+@pytest.mark.parametrize("T,E,topk", [(1, 2, 1), (2, 3, 2), (9, 8, 1), (40, 3, 2)])
+def test_moe_of_more_row_tiles_than_share_sums(T, E, topk):
+    """65 tiles of 128 rows in down: no tile is shared by several clusters"""
+    args = moe_inputs(T, E, 8208, 32, 31)
+    check_moe(fp8_moe(*args, topk), *args, topk)
+
+
+@pytest.mark.parametrize("T,E,topk", [(1, 16, 4), (8, 16, 4), (9, 16, 4), (17, 16, 2), (64, 256, 8), (64, 16, 4)])
+def test_moe_error_word_stays_clear(T, E, topk):
+    args = moe_inputs(T, E, 640, 144, 32)
+    check_moe(fp8_moe(*args, topk), *args, topk)
+
+
+def test_layer_error_words_stay_clear():
+    layer = Layer(48, seed=33)
+    layer.run()
+    layer.check()
+    assert layer.wm.check() == 0
+
+
+def test_library_functions_by_their_names():
+    """the sharq_fp8_* functions on plain addresses write the bits that the torch conveniences return"""
+    T, K, D, stream = 12, 272, 136, torch.cuda.current_stream().cuda_stream
+    W, X, R = (bf(synthetic.weights(41, K, D)), bf(synthetic.activations(42, T, K)), bf(synthetic.activations(43, T, K)))
+    G = bf(synthetic.gamma(44, K))
+
+    def buffer(n):
+        return torch.zeros(n, dtype=torch.uint8, device="cuda")
+
+    wb, ab = buffer(sq.sharq_fp8_weight_bytes(K, D)), buffer(sq.sharq_fp8_act_bytes(T, K))
+    w, a = sq.sharq_fp8_weight_view(wb.data_ptr(), K, D), sq.sharq_fp8_act_view(ab.data_ptr(), T, K)
+    sq.sharq_fp8_pack_weight(W.data_ptr(), w, stream)
+    weight, act = sq.Fp8Weight(W), sq.Fp8Act(T, K)
+    assert torch.equal(wb[:K * D], weight.codes.view(torch.uint8).reshape(-1))
+    off = w.scales - w.codes
+    assert torch.equal(wb[off:off + weight.scales.numel() * 4].view(torch.float32), weight.scales.reshape(-1))
+
+    def same():
+        b = O.blocks(K)
+        sc = ab[a.scales - a.codes:][:4 * b * a.lds].view(torch.float32).view(b, a.lds)[:, :T].t()
+        return torch.equal(ab[:T * K], act.codes.view(torch.uint8).reshape(-1)) and torch.equal(sc, act.scales)
+
+    sq.sharq_fp8_prep(X.data_ptr(), K, G.data_ptr(), 1e-5, a, stream)
+    act.prep(X, G)
+    assert same()
+    gu = torch.cat([X, R], 1)
+    sq.sharq_fp8_prep_silu_mul(gu.data_ptr(), 2 * K, gu.data_ptr() + 2 * K, 2 * K, a, stream)
+    act.prep_silu_mul(gu[:, :K], gu[:, K:])
+    assert same()
+    out = torch.empty_like(R)
+    sq.sharq_fp8_prep_residual(X.data_ptr(), K, R.data_ptr(), K, out.data_ptr(), K, G.data_ptr(), 1e-5, a, stream)
+    act.prep_residual(X, R, R, G)
+    assert same() and torch.equal(out, R)
+    ws, y = buffer(sq.sharq_fp8_linear_workspace_bytes(T, K, D)), torch.empty(T, D, device="cuda")
+    sq.sharq_fp8_linear(a, w, y.data_ptr(), D, sq.SHARQ_OUT_F32, ws.data_ptr(), ws.numel(), stream)
+    assert torch.equal(y, sq.fp8_linear(act, weight, out_dtype=torch.float32))
+    x, lg, *parts = (t.cuda() for t in moe_inputs(T, 6, 256, 64, 45))
+    w13, w2 = sq.Fp8Weight.from_parts(*parts[:2]), sq.Fp8Weight.from_parts(*parts[2:])
+    wm, y = buffer(sq.sharq_fp8_moe_workspace_bytes(T, 2, 256, 64, 6)), torch.empty_like(x)
+    ids, p = torch.empty(T, 2, dtype=torch.int32, device="cuda"), torch.empty(T, 2, device="cuda")
+    sq.sharq_fp8_moe(x.data_ptr(), 256, lg.data_ptr(), 6, T, 2, 1, w13.view, w2.view, y.data_ptr(), 256, ids.data_ptr(),
+                     p.data_ptr(), wm.data_ptr(), wm.numel(), stream)
+    for got, want in zip((y, ids, p), sq.fp8_moe(x, lg, w13, w2, 2, return_routing=True)):
+        assert torch.equal(got, want)
+    assert sq.sharq_check_status(ws.data_ptr(), stream) == 0 and sq.sharq_check_status(wm.data_ptr(), stream) == 0
+    with pytest.raises(sq.SharqError):
+        sq.sharq_fp8_linear(a, w, y.data_ptr(), D, sq.SHARQ_OUT_F32, ws.data_ptr(), 16, stream)
+
+
+def test_captured_layers_replayed_at_once():
+    """two graphs with a workspace each, replayed side by side on two streams"""
+    layers, graphs, want = [Layer(16, seed=51), Layer(64, seed=52)], [], []
+    for la in layers:
+        la.run()
+        torch.cuda.synchronize()
+        want.append(la.outputs())
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            la.run()
+        graphs.append(g)
+    for la in layers:
+        for t in (la.h, la.gu, la.down, la.y):
+            t.fill_(float("nan"))
+    streams = [torch.cuda.Stream() for _ in layers]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    for la, w in zip(layers, want):
+        assert all(torch.equal(a, b) for a, b in zip(la.outputs(), w))
+        assert la.ws.check() == 0 and la.wm.check() == 0
+
+
+def test_beside_the_fp4_path_on_another_stream():
+    """both paths' kernels hold TMEM and clusters on the same SMs"""
+    T, K, D = 600, 1024, 2048
+    fp4 = sq.PackedWeight(bf(synthetic.weights(61, K, D)))
+    x, gamma = bf(synthetic.activations(62, T, K)), bf(synthetic.gamma(63, K))
+    rows = {n: (sq.PreparedAct(n, K), sq.Workspace(n, K, D)) for n in (8, T)}
+
+    def four(stream=None):
+        return [sq.linear(a.prep(x[:n], gamma, 1e-5, stream=stream), fp4, ws=ws, stream=stream)
+                for n, (a, ws) in rows.items()]
+
+    layers = [Layer(n, seed=64 + n) for n in (8, 64)]
+    want4 = four()
+    for la in layers:
+        la.run()
+    torch.cuda.synchronize()
+    want8 = [la.outputs() for la in layers]
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(20):
+        with torch.cuda.stream(a):
+            got4 = four(a)
+        for la in layers:
+            la.run(stream=b)
+    torch.cuda.synchronize()
+    assert all(torch.equal(g, w) for g, w in zip(got4, want4))
+    for la, w in zip(layers, want8):
+        assert all(torch.equal(g, v) for g, v in zip(la.outputs(), w)) and la.wm.check() == 0
+    assert all(ws.check() == 0 for _, ws in rows.values())
+
+
+FIRST = """
+import torch
+import sparse_activation_quantization_b200 as sq
+from tests.test_gpu_fp8 import Layer
+layer, g = Layer(%d, seed=71), torch.cuda.CUDAGraph()
+torch.cuda.synchronize()
+with torch.cuda.graph(g):
+    layer.run()
+layer.y.fill_(float("nan"))
+g.replay()
+layer.check()
+assert layer.wm.check() == 0
+print("captured first")
+"""
+
+
+@pytest.mark.parametrize("T", [3, 40])
+def test_first_call_of_a_process_may_be_captured(T):
+    """what a kernel's first launch looks up (attributes, resident clusters) is allowed while a stream is captured"""
+    r = subprocess.run([sys.executable, "-c", FIRST % T], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "captured first" in r.stdout, r.stderr[-2000:]
