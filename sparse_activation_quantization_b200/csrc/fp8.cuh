@@ -1,6 +1,6 @@
 // fp8.cuh - device helpers of the 8-bit (E4M3, block-scaled) path: format
-// conversion, the legacy warp-level matrix instructions that stream a weight
-// once, tensor-map copies and the 8-bit tcgen05 MMA.
+// conversion, bounded waits, tensor-map copies and the 8-bit tcgen05 MMA; and
+// what its launchers share.
 #pragma once
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -90,10 +90,6 @@ __device__ __forceinline__ bool elect_one() {
       "selp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(p));
   return p != 0;
-}
-
-__device__ __forceinline__ void prefetch_l1(const void* p) {
-  asm volatile("prefetch.global.L1 [%0];" ::"l"(p) : "memory");
 }
 
 __device__ __forceinline__ void record_error_word(int* err, int code) {

@@ -324,16 +324,18 @@ cudaError_t launch_norm(PrepArgs& a, int grid, int block, cudaStream_t stream) {
 }
 
 template <int kKind>
-cudaError_t launch_kind(PrepArgs& a, cudaStream_t stream) {
+cudaError_t launch_quant(PrepArgs& a, const Device* d, cudaStream_t stream) {
   void* args[] = {&a};
-  const Device* d = device();
-  if (!d) return cudaErrorInvalidDevice;
-  if (!a.gamma) {
-    // 16 blocks a CTA and step; kQuantCtas CTAs reside on an SM
-    const long long want = ((long long)a.T * blocks_of(a.K) + 15) / 16, most = (long long)d->sms * kQuantCtas;
-    return launch_pdl((const void*)fp8_quant_kernel<kKind>, dim3((unsigned)(want < most ? want : most)), dim3(256), 0,
-                      1, stream, args);
-  }
+  // 16 blocks a CTA and step; kQuantCtas CTAs reside on an SM
+  const long long want = ((long long)a.T * blocks_of(a.K) + 15) / 16, most = (long long)d->sms * kQuantCtas;
+  return launch_pdl((const void*)fp8_quant_kernel<kKind>, dim3((unsigned)(want < most ? want : most)), dim3(256), 0, 1,
+                    stream, args);
+}
+
+template <int kKind>
+cudaError_t launch_rows(PrepArgs& a, const Device* d, cudaStream_t stream) {
+  if (!a.gamma) return launch_quant<kKind>(a, d, stream);
+  void* args[] = {&a};
   const int vecs = (a.K + 7) / 8;
   // Short rows: a warp each, four to a CTA.
   if (vecs <= 128) {
@@ -461,9 +463,11 @@ cudaError_t launch_prep(int kind, const void* x, long long ldx, const void* b, l
   a.K = K;
   a.lds = lds;
   a.eps = eps;
-  if (kind == kResidual) return launch_kind<kResidual>(a, stream);
-  if (kind == kSwiglu) return launch_kind<kSwiglu>(a, stream);
-  return launch_kind<kPlain>(a, stream);
+  const Device* d = device();
+  if (!d) return cudaErrorInvalidDevice;
+  if (kind == kSwiglu) return launch_quant<kSwiglu>(a, d, stream);  // has no norm
+  if (kind == kResidual) return launch_rows<kResidual>(a, d, stream);
+  return launch_rows<kPlain>(a, d, stream);
 }
 
 cudaError_t launch_pack(const void* W, int K, int D, int E, uint8_t* codes, float* scales, cudaStream_t stream) {
