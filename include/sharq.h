@@ -466,7 +466,8 @@ int sharq_fp8_linear(const sharq_fp8_act *a, const sharq_fp8_weight *w, void *d_
  * sharq_fp8_moe - a whole mixture-of-experts layer for a few tokens (decode),
  * in two kernels up to 8 tokens and one or two more above (the choice of the
  * experts; with more than 4 tokens an expert on average, h's operand form).
- * Larger batches belong to a grouped GEMM.
+ * Larger batches are refused: the grouped linear above is the FP4 path's, an
+ * 8-bit one is not there.
  *   chosen(t): the topk largest of d_logits[t][0..E-1] (float32, row stride
  *     ldl), equal logits by the lower index.
  *   p(t, j): softmax over the chosen logits (renormalize != 0) or the chosen

@@ -492,10 +492,12 @@ __global__ void __launch_bounds__(Tile::kThreads, 1)
 //   warp 1      TMEM allocation; in the even CTA one thread issues the MMAs into
 //               four 128-column TMEM buffers, half a tile's columns each; its
 //               commits arrive on both CTAs' barriers
-// The MMAs of a block take about 520 cycles.  Adding its 256 columns takes each
-// warp scheduler 256 cycles of the FMA pipe, and the plain loop below (wait, read
-// 32 columns, add them) 390 in all, two warps taking turns.  (Reading the next
-// piece while one is added needs 192 registers of values alone and spills: 650.)
+// The MMAs of a block take 575 cycles by themselves.  Adding its 256 columns
+// takes each warp scheduler 256 cycles of the FMA pipe, and the plain loop below
+// (wait, read 64 columns, add them) 390 in all, two warps taking turns.  (Reading
+// the next piece while one is added spills.)  Together they take 800 a block, and
+// each tile 2650 more: 2100 for its store, 550 until the next tile's first buffer
+// is full.  8192 x 3584 x 37888: 64 tiles a pair, 1.61 million cycles, 1008 us.
 // A buffer's way round (sums' release, across the pair, MMAs, commit, read) takes
 // more than 1200 cycles, so there are four of them.
 // Waits acquire at CTA scope: what they guard is TMEM (ordered by the tcgen05

@@ -258,7 +258,9 @@ def _workspace(ws, device):
 
 def fp8_linear(act, weight, out_dtype=None, out=None, ws=None, stream=None):
     """Y = X W through sharq_fp8_linear; act: Fp8Act, weight: Fp8Weight.  `out`
-    (bf16 or float32, rows contiguous) may be a column slice of a wider tensor."""
+    (bf16 or float32, rows contiguous) may be a column slice of a wider tensor.
+    ws: the Fp8Workspace whose check() tells of a wait that ran out; without one
+    the call makes its own, whose error word is gone with it."""
     if weight.device != act.device:
         raise ValueError(f"weight on {weight.device}, activation on {act.device}")
     device = act.device
@@ -285,7 +287,8 @@ def fp8_moe(x, logits, w13, w2, topk, renormalize=True, out=None, ws=None, retur
     x: bf16 [T, H], T <= 64; logits: float32 [T, E], the router's output;
     w13: Fp8Weight of codes [E, 2 I, H], gate rows first; w2: of [E, H, I].
     Returns y (bf16 [T, H]; `out` may be x), with return_routing also the chosen
-    experts (int32 [T, topk]) and their weights (float32 [T, topk])."""
+    experts (int32 [T, topk]) and their weights (float32 [T, topk]).  ws as in
+    fp8_linear, from Fp8Workspace.for_moe."""
     device = w13.device
     if w2.device != device:
         raise ValueError(f"w2 on {w2.device}, w13 on {device}")
