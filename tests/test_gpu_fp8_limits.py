@@ -261,3 +261,118 @@ def test_first_call_of_a_process_may_be_captured(T):
     """what a kernel's first launch looks up (attributes, resident clusters) is allowed while a stream is captured"""
     r = subprocess.run([sys.executable, "-c", FIRST % T], cwd=ROOT, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and "captured first" in r.stdout, r.stderr[-2000:]
+
+
+# ------------------------------------------------- the largest of each size ---
+
+
+@pytest.mark.parametrize("T,K,D", [(1, 131072, 40), (40, 131072, 130), (70, 131072, 24), (300, 131072, 140),  # sums of 1024 blocks
+                                   (1, 16, 262144), (65, 16, 262144),
+                                   (300001, 16, 9), (70000, 144, 16)])
+def test_linear_of_the_largest_sizes(T, K, D):
+    x, xs, w, ws = operands(T, K, D, 3)
+    act = sq.Fp8Act.from_parts(x.cuda(), xs.cuda())
+    wt = sq.Fp8Weight.from_parts(w.cuda(), ws.cuda())
+    work = sq.Fp8Workspace.for_linear(T, K, D)
+    y = sq.fp8_linear(act, wt, out_dtype=torch.float32, ws=work)
+    ref, bound = linear_reference(x, xs, w, ws)
+    check_linear(y, ref, bound, torch.float32)
+    assert work.check() == 0
+
+
+@pytest.mark.parametrize("T,K", [(2, 131072), (70001, 16), (70001, 272)])
+def test_prep_of_the_largest_sizes(T, K):
+    x, r, gamma = synthetic.activations(91, T, K), synthetic.activations(92, T, K), synthetic.gamma(93, K)
+    act, codes, scales = make_act(T, K)
+    X, R, G = bf(x), bf(r), bf(gamma)
+    act.prep(X)
+    q, s = O.quant(x)
+    assert np.array_equal(act.scales.cpu().numpy(), s) and np.array_equal(f64(act.codes.float()), q)
+    act.prep(X, G)
+    check_quant(act, O.rms_norm(x, gamma, np.float32(1e-5)), norm_delta(K))
+    act.prep_silu_mul(X, R)
+    check_quant(act, O.silu(x) * r, (2 + 1.2 * 88 + 8) * 2.0 ** -23)
+    act.prep_residual(X, R, R, G)
+    h = (torch.from_numpy(x) + torch.from_numpy(r)).bfloat16()
+    assert torch.equal(R.cpu(), h)
+    check_quant(act, O.rms_norm(h.float().numpy(), gamma, np.float32(1e-5)), norm_delta(K))
+    check_untouched(act, codes, scales)
+
+
+@pytest.mark.parametrize("E,K,D", [(1, 131072, 17), (1, 16, 262144), (4096, 16, 3), (3, 144, 70000)])
+def test_pack_of_the_largest_sizes(E, K, D):
+    W = synthetic.weights(94, E * K, D).reshape(E, K, D)
+    w = sq.Fp8Weight(bf(W))
+    codes, scales = f64(w.codes.float()), w.scales.cpu().numpy()
+    for e in range(0, E, max(1, E // 8)):
+        q, s = O.pack(W[e])
+        assert np.array_equal(scales[e], s) and np.array_equal(codes[e], q)
+
+
+@pytest.mark.parametrize("T,E,topk,Hd,I", [(1, 1, 1, 131072, 16), (9, 3, 1, 131072, 16), (33, 2, 2, 131072, 16),
+                                           (1, 2, 1, 16, 131072), (9, 4, 1, 16, 131072), (34, 2, 1, 16, 131072)])
+def test_moe_of_the_largest_sizes(T, E, topk, Hd, I):
+    args = moe_inputs(T, E, Hd, I, 95)
+    if I == 131072:  # sums of 131072 products: keeps |W2| within what check_moe takes
+        args = (*args[:5], args[5] * 2.0 ** -4)
+    check_moe(fp8_moe(*args, topk), *args, topk)
+
+
+def test_rows_further_apart_than_32_bits_say():
+    """strides of more than 2^31 elements: input, output and in-place stream"""
+    far, T, K, D = 2 ** 31 + 8, 3, 272, 24
+    big = torch.empty(2 * far + K, dtype=torch.bfloat16, device="cuda")
+    x, r = synthetic.activations(96, T, K), synthetic.activations(97, T, K)
+    X = big.as_strided((T, K), (far, 1))
+    X.copy_(bf(x))
+    act, near = sq.Fp8Act(T, K), sq.Fp8Act(T, K)
+    act.prep(X)
+    near.prep(bf(x))
+    assert torch.equal(act.codes.view(torch.uint8), near.codes.view(torch.uint8)) and torch.equal(act.scales, near.scales)
+    G = bf(synthetic.gamma(98, K))
+    act.prep_residual(bf(r), X, X, G)  # the stream is updated where it lies
+    R = bf(x)
+    near.prep_residual(bf(r), R, R, G)
+    assert torch.equal(X, R) and torch.equal(act.codes.view(torch.uint8), near.codes.view(torch.uint8))
+    w = sq.Fp8Weight(bf(synthetic.weights(99, K, D)))
+    out = big.as_strided((T, D), (far, 1))
+    sq.fp8_linear(near, w, out=out)
+    assert torch.equal(out, sq.fp8_linear(near, w))
+    x, lg, *p = (t.cuda() for t in moe_inputs(3, 4, K, 48, 101))
+    a, b = sq.Fp8Weight.from_parts(*p[:2]), sq.Fp8Weight.from_parts(*p[2:])
+    want = sq.fp8_moe(x, lg, a, b, 2)
+    X.copy_(x)
+    assert torch.equal(sq.fp8_moe(X, lg, a, b, 2, out=X), want)
+    del big, X
+    torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("E,topk", [(129, 1), (300, 16), (512, 3)])
+def test_moe_without_renormalizing_over_many_experts(E, topk):
+    args = moe_inputs(7, E, 128, 32, 102, spread=3.0)
+    check_moe(fp8_moe(*args, topk, renormalize=False), *args, topk, renormalize=False)
+
+
+def test_two_threads_call_at_once():
+    """the host side's tables (attributes, resident clusters) are filled by whoever comes first"""
+    code = """
+import threading, torch
+from tests.test_gpu_fp8 import Layer
+layers = [Layer(5, seed=111), Layer(40, seed=112)]
+streams = [torch.cuda.Stream() for _ in layers]
+torch.cuda.synchronize()
+def work(la, s):
+    torch.cuda.set_device(0)
+    for _ in range(30):
+        la.run(stream=s)
+ts = [threading.Thread(target=work, args=a) for a in zip(layers, streams)]
+[t.start() for t in ts]
+[t.join() for t in ts]
+torch.cuda.synchronize()
+for la in layers:
+    la.check()
+    assert la.wm.check() == 0
+print("both right")
+"""
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "both right" in r.stdout, r.stderr[-2000:]
